@@ -411,6 +411,141 @@ lca_status lca_decode_noalloc(int B, int H, int d_c, int d_r, lca_dtype dt, cons
                               const void *q_r, const void *c_kv, const void *k_r, int64_t L, int g,
                               int w, float *out, int32_t *anchor_idx, void *stream);
 
+/*
+ * Drafted tokens and eviction.  The page decodes one token a step over a cache
+ * that only grows; these four calls serve the steps around it: several drafted
+ * tokens of a sequence attended at once (speculative decoding), the attention
+ * weight that each cached token has received added up over steps, the rows
+ * that an eviction by those sums keeps, and the kept (or accepted) rows moved
+ * together.  They share one description of the cache:
+ *   c_pool, k_pool  device, plan dtype: rows of d_c and of d_r, num_pages pages of
+ *                   page_size rows, num_pages page_size < 2^31
+ *   block_table     device int32 [B][max_pages] as for lca_decode_paged (page_size a
+ *                   positive multiple of 64); NULL for a contiguous cache: sequence b's
+ *                   rows are b page_size .. b page_size + page_size - 1 (page_size its
+ *                   capacity, any positive number; num_pages >= B; max_pages >= 1 is
+ *                   not read)
+ *   seq_lens        device int32 [B]: n_b >= 0 cached tokens, positions 0 .. n_b - 1
+ *   n_draft = T     1 .. 64 query rows (nodes) a sequence has room for
+ *   draft_lens      device int32 [B]: d_b in 0 .. T drafted tokens, at positions
+ *                   n_b .. n_b + d_b - 1 of the cache (their rows are written there
+ *                   before the call); NULL: T for every sequence
+ *   mask            device uint64 [B][T]: bit j of word i says that node i sees node j
+ *                   (usually its ancestors and itself; bits from d_b on are not read);
+ *                   NULL: a chain, node i sees nodes 0 .. i
+ *   q_c, q_r        device, plan dtype: [B][T][H][d_c] and [B][T][H][d_r], the softmax
+ *                   scale folded in as for lca_decode
+ * n_b + d_b may not exceed min(max_L, max_pages page_size) (contiguous: min(max_L,
+ * page_size)).  Lengths, masks and table entries stay on the device; the calls are
+ * asynchronous, allocate nothing, and can be captured in a CUDA graph.  A length
+ * out of range makes its sequence empty (and see each call); a used table entry
+ * outside [0, num_pages) is read as page 0 and never written.  Either raises
+ * LCA_ERR_DEVICE_INPUT from the next lca_get_device_error.  Rows of no token, and
+ * drafted rows that a node does not see, may hold anything, NaN included.
+ * Unlike the plan's own workspace, the one given here belongs to the call: two
+ * streams, or two captured graphs, that each bring their own may use one plan at
+ * once.
+ */
+
+/* Bytes of workspace that lca_tree_decode and lca_attn_mass want for T = n_draft
+ * (256-byte aligned, no initial contents, any use after the call); -1 for a NULL
+ * plan or n_draft outside 1 .. 64. */
+int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
+
+/*
+ * Attention of drafted tokens: for node i < d_b and head h, with x_t = q_c.c_t +
+ * q_r.k_t over the cached tokens and the drafted ones that node i sees,
+ *   lse = log sum_t e^{x_t},  out = sum_t e^{x_t - lse} c_t.
+ * A node that sees nothing (n_b = 0 and an empty mask word) gives out = 0, lse = -inf.
+ * T = 1 is the decode step over a cache of n_b + 1 rows.
+ *   out        device, plan dtype [B][T][H][d_c] (rounded once, from fp32)
+ *   lse        device fp32 [B][T][H], natural logarithm; NULL: not wanted
+ * Rows of nodes i >= d_b are left as they were; those of a sequence whose lengths
+ * are out of range become NaN.  Where a drafted row holds an infinity or NaN, the
+ * nodes that see it give NaN and the others are not touched by it.
+ * bf16 with (d_c, d_r) = (512, 64) runs a tcgen05 kernel (softmax weights rounded
+ * to bf16 for their product with the values, everything else fp32); other plans the
+ * CUDA-core kernel.  LCA_OPT_FORCE_SIMT and LCA_OPT_KERNEL 0 .. 2 choose as for
+ * lca_decode.
+ * Errors: LCA_ERR_INVALID_ARG (NULL plan, q, pools, seq_lens, out or workspace;
+ * n_draft outside 1 .. 64; sizes below 1; a paged page_size not a multiple of 64; a
+ * contiguous num_pages < B; workspace_bytes below lca_tree_workspace),
+ * LCA_ERR_UNSUPPORTED (2^31 rows or more, B T H >= 2^31, B > 65535, no kernel),
+ * LCA_ERR_ALIGNMENT (q, pools, out: 16 bytes; workspace: 256; mask: 8; the rest: 4),
+ * LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.
+ */
+lca_status lca_tree_decode(lca_plan *plan, const void *q_c, const void *q_r, int n_draft,
+                           const void *c_pool, const void *k_pool, int64_t num_pages, int page_size,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *seq_lens,
+                           const int32_t *draft_lens, const uint64_t *mask, void *out, float *lse,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * The attention weight that each token received, summed over heads and nodes and
+ * added to what it had: with x as above and lse as lca_tree_decode gave it,
+ *   scores[b][t] = decay prev[b][t] + sum_{i,h} e^{x_t - lse[b][i][h]}   t < n_b,
+ *   scores[b][t] = sum_{i,h : i sees t} e^{x_t - lse[b][i][h]}           the drafted t.
+ *   lse        device fp32 [B][T][H]; a row of +inf or -inf adds nothing (a caller sets
+ *              the rows of rejected nodes to +inf)
+ *   prev       device fp32 [B][score_stride]; NULL: zeros.  May be `scores` itself.
+ *              Not read where decay is 0.
+ *   scores     device fp32 [B][score_stride]; score_stride also bounds n_b + d_b.
+ *              Positions from n_b + d_b on, and every position of a sequence whose
+ *              lengths are out of range, are left as they were.
+ * The sums are formed in fp32 in a fixed order: the same call gives the same bits.
+ * Kernels, options and errors as for lca_tree_decode (NULL lse or scores and
+ * score_stride < 1 too are LCA_ERR_INVALID_ARG).
+ */
+lca_status lca_attn_mass(lca_plan *plan, const void *q_c, const void *q_r, int n_draft,
+                         const void *c_pool, const void *k_pool, int64_t num_pages, int page_size,
+                         const int32_t *block_table, int64_t max_pages, const int32_t *seq_lens,
+                         const int32_t *draft_lens, const uint64_t *mask, const float *lse,
+                         const float *prev, float decay, float *scores, int64_t score_stride,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Which rows an eviction keeps.  Of the n_b rows of a sequence with n_b > budget:
+ * the first n_sink, the last n_recent, and as many of those between, with the
+ * largest sums, as make `budget`; equal sums (0 and -0 are) go to the lower row, NaN
+ * counts as the smallest.  With n_b <= budget every row is kept.
+ *   scores     device fp32 [B][score_stride]; rows from n_b on are not read
+ *   seq_lens   device int32 [B]: 0 <= n_b <= min(max_L, score_stride)
+ *   kept       device int32 [B][budget]: the kept rows of each sequence, rising;
+ *              entries from kept_lens[b] on are left as they were
+ *   kept_lens  device int32 [B]: min(n_b, budget); 0 where n_b is out of range
+ * Only B, max_L and the device of the plan count.  Errors: LCA_ERR_INVALID_ARG (NULL
+ * pointers, score_stride < 1, budget < 1, n_sink or n_recent < 0 or their sum above
+ * budget), LCA_ERR_ALIGNMENT (4 bytes), LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.
+ */
+lca_status lca_evict_select(lca_plan *plan, const float *scores, int64_t score_stride,
+                            const int32_t *seq_lens, int64_t n_sink, int64_t n_recent,
+                            int64_t budget, int32_t *kept, int32_t *kept_lens, void *stream);
+
+/*
+ * Move rows together, in place: row dst0[b] + j of sequence b becomes its row
+ * src[b][j] for j < n_src[b], in C_KV, K_R and, if given, the sums.  With the rows
+ * of lca_evict_select (dst0 NULL) this is the eviction; with dst0 = n_b and src the
+ * positions of an accepted path of drafted tokens it commits the path.  The order of
+ * the rows is kept, as the groups and windows of lca_decode need.
+ *   src        device int32 [B][src_stride]: strictly rising, dst0[b] + j <= src[b][j] <
+ *              the bound on lengths
+ *   n_src      device int32 [B]: 0 .. src_stride
+ *   dst0       device int32 [B]; NULL: 0
+ *   scores     device fp32 [B][score_stride], moved alike (score_stride then also
+ *              bounds positions); NULL: none
+ * No page may be listed twice among the rows that move or are moved to (pages
+ * shared by sequences must lie below dst0).  An entry of src that breaks its bounds
+ * or order, or whose page is out of range, is not moved, a sequence whose n_src or
+ * dst0 is out of range is left alone; either raises LCA_ERR_DEVICE_INPUT.
+ * Errors: LCA_ERR_INVALID_ARG (as above; src_stride outside 1 .. 2^31 - 1),
+ * LCA_ERR_UNSUPPORTED, LCA_ERR_ALIGNMENT (pools 16 bytes, the rest 4),
+ * LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.
+ */
+lca_status lca_cache_compact(lca_plan *plan, void *c_pool, void *k_pool, int64_t num_pages,
+                             int page_size, const int32_t *block_table, int64_t max_pages,
+                             const int32_t *src, int64_t src_stride, const int32_t *n_src,
+                             const int32_t *dst0, float *scores, int64_t score_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "liblca.so")
 CHECKED_LIB_PATH = os.path.join(HERE, "liblca_checked.so")
 
 LCA_OK = 0
+LCA_ERR_INVALID_ARG = 1
 LCA_ERR_UNSUPPORTED = 2
 LCA_ERR_DEVICE_TIMEOUT = 5
 STATUS = {0: "LCA_OK", 1: "LCA_ERR_INVALID_ARG", 2: "LCA_ERR_UNSUPPORTED", 3: "LCA_ERR_ALIGNMENT",
@@ -32,7 +33,9 @@ EXPORTS = ["lca_plan_create", "lca_plan_destroy", "lca_plan_set", "lca_decode", 
            "lca_plan_kernel", "lca_plan_set_timing_event", "lca_decode_noalloc", "lca_condense",
            "lca_stored_rows", "lca_build_stored", "lca_decode_stored", "lca_slice_groups",
            "lca_decode_partial", "lca_merge_partials", "lca_get_device_error_site", "lca_decode_paged",
-           "lca_prefill_paged", "lca_decode_gqa"]
+           "lca_prefill_paged", "lca_decode_gqa", "lca_tree_workspace", "lca_tree_decode", "lca_attn_mass",
+           "lca_evict_select", "lca_cache_compact"]
+MAX_DRAFT = 64    # nodes of a draft tree: one mask word each
 
 
 class LcaError(RuntimeError):
@@ -82,11 +85,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.lca_decode_paged.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, i64, vp, i32, i32, vp, vp, i64, vp]
     lib.lca_prefill_paged.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, i64, i64, i32, i32, vp, vp, i64, vp]
     lib.lca_decode_gqa.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp]
+    cache = [vp, vp, i64, i32, vp, i64]             # c_pool, k_pool, num_pages, page_size, block_table, max_pages
+    lib.lca_tree_workspace.argtypes = [vp, i32]
+    lib.lca_tree_workspace.restype = i64
+    lib.lca_tree_decode.argtypes = [vp, vp, vp, i32, *cache, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.lca_attn_mass.argtypes = [vp, vp, vp, i32, *cache, vp, vp, vp, vp, vp, ctypes.c_float, vp, i64, vp, i64, vp]
+    lib.lca_evict_select.argtypes = [vp, vp, i64, vp, i64, i64, i64, vp, vp, vp]
+    lib.lca_cache_compact.argtypes = [vp, *cache, vp, i64, vp, vp, vp, i64, vp]
     for name in ("lca_plan_create", "lca_plan_destroy", "lca_plan_set", "lca_decode", "mla_decode",
                  "lca_decode_host", "lca_get_device_error", "lca_plan_kernel",
                  "lca_plan_set_timing_event", "lca_decode_noalloc", "lca_condense",
                  "lca_build_stored", "lca_decode_stored", "lca_decode_partial", "lca_merge_partials",
-                 "lca_decode_paged", "lca_prefill_paged", "lca_decode_gqa"):
+                 "lca_decode_paged", "lca_prefill_paged", "lca_decode_gqa", "lca_tree_decode", "lca_attn_mass",
+                 "lca_evict_select", "lca_cache_compact"):
         getattr(lib, name).restype = i32
     if path == LIB_PATH:
         _lib = lib
@@ -104,6 +115,14 @@ def _check(status: int, what: str) -> None:
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
+
+
+def _expect(what: str, t, dtype, *shape) -> None:
+    """`t` is a contiguous CUDA tensor of this type and shape (None: any size); LCA_ERR_INVALID_ARG otherwise."""
+    if (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape)
+            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise LcaError(LCA_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}; "
+                       f"wanted a contiguous CUDA tensor of {dtype} {tuple('*' if n is None else n for n in shape)}")
 
 
 def _stream_handle(stream) -> int | None:
@@ -238,6 +257,114 @@ class Plan:
         _check(self._lib.lca_decode_gqa(self._h, _ptr(q), _ptr(k_cache), _ptr(v_cache), L, n_kv_heads, g, w,
                                         _ptr(out), _ptr(anchor), _stream_handle(stream)), "lca_decode_gqa")
 
+    # ------------------------------------------------------------ drafted tokens and eviction
+
+    def _elem(self):
+        import torch
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+    def _cache_args(self, c_pool, k_pool, page_size: int, block_table):
+        """The cache arguments of the C calls, checked: pools [rows, d] (or [B, capacity, d]) and an int32
+        block_table [B, max_pages], or None for a contiguous cache with page_size rows a sequence."""
+        import torch
+        if c_pool.dim() == 3:
+            c_pool, k_pool = c_pool.flatten(0, 1), k_pool.flatten(0, 1)
+        rows = c_pool.shape[0]
+        _expect("c_pool", c_pool, self._elem(), rows, self.d_c)
+        _expect("k_pool", k_pool, self._elem(), rows, self.d_r)
+        if block_table is not None:
+            _expect("block_table", block_table, torch.int32, self.B, None)
+        return (_ptr(c_pool), _ptr(k_pool), rows // page_size if page_size > 0 else 0, page_size, _ptr(block_table),
+                1 if block_table is None else block_table.shape[1])
+
+    def _draft_args(self, q_c, q_r, seq_lens, draft_lens, mask):
+        import torch
+        T = q_c.shape[1]
+        _expect("q_c", q_c, self._elem(), self.B, T, self.H, self.d_c)
+        _expect("q_r", q_r, self._elem(), self.B, T, self.H, self.d_r)
+        _expect("seq_lens", seq_lens, torch.int32, self.B)
+        if draft_lens is not None:
+            _expect("draft_lens", draft_lens, torch.int32, self.B)
+        if mask is not None:
+            _expect("mask", mask, torch.int64, self.B, T)
+        return T
+
+    def tree_workspace(self, n_draft: int, stream=None):
+        """A workspace for tree_decode and attn_mass with up to n_draft drafted tokens a sequence: keep one per
+        stream (or captured graph) that runs at the same time as others, or let each call take its own."""
+        import torch
+        size = int(self._lib.lca_tree_workspace(self._h, n_draft))
+        if size < 0:
+            raise LcaError(LCA_ERR_INVALID_ARG, f"tree_workspace: n_draft {n_draft} outside 1 .. {MAX_DRAFT}")
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
+
+    def tree_decode(self, q_c, q_r, c_pool, k_pool, page_size: int, block_table, seq_lens, out, lse=None, mask=None,
+                    draft_lens=None, workspace=None, stream=None) -> None:
+        """lca_tree_decode: attention of drafted tokens over the cache.  q_c [B,T,H,d_c], q_r [B,T,H,d_r]; pools
+        and block_table as for decode_paged, or block_table None and pools [B, page_size, d]; seq_lens, draft_lens
+        int32 [B]; mask int64 [B,T] (see tree_mask), None for a chain; out [B,T,H,d_c] of the plan's type, lse
+        [B,T,H] fp32 or None."""
+        import torch
+        T = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
+        cache = self._cache_args(c_pool, k_pool, page_size, block_table)
+        _expect("out", out, self._elem(), self.B, T, self.H, self.d_c)
+        if lse is not None:
+            _expect("lse", lse, torch.float32, self.B, T, self.H)
+        if workspace is None:
+            workspace = self.tree_workspace(T, stream)
+        _check(self._lib.lca_tree_decode(self._h, _ptr(q_c), _ptr(q_r), T, *cache, _ptr(seq_lens), _ptr(draft_lens),
+                                         _ptr(mask), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                         _stream_handle(stream)), "lca_tree_decode")
+
+    def attn_mass(self, q_c, q_r, c_pool, k_pool, page_size: int, block_table, seq_lens, lse, scores, prev=None,
+                  decay: float = 1.0, mask=None, draft_lens=None, workspace=None, stream=None) -> None:
+        """lca_attn_mass: scores [B, stride] fp32 = decay * prev + the attention weight each token receives from
+        these queries (lse from tree_decode; +inf leaves a row out).  prev may be scores, None stands for zeros."""
+        import torch
+        T = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
+        cache = self._cache_args(c_pool, k_pool, page_size, block_table)
+        _expect("lse", lse, torch.float32, self.B, T, self.H)
+        _expect("scores", scores, torch.float32, self.B, None)
+        if prev is not None:
+            _expect("prev", prev, torch.float32, self.B, scores.shape[1])
+        if workspace is None:
+            workspace = self.tree_workspace(T, stream)
+        _check(self._lib.lca_attn_mass(self._h, _ptr(q_c), _ptr(q_r), T, *cache, _ptr(seq_lens), _ptr(draft_lens),
+                                       _ptr(mask), _ptr(lse), _ptr(prev), float(decay), _ptr(scores),
+                                       scores.shape[1], _ptr(workspace), workspace.numel(), _stream_handle(stream)),
+               "lca_attn_mass")
+
+    def evict_select(self, scores, seq_lens, n_sink: int, n_recent: int, kept, kept_lens, stream=None) -> None:
+        """lca_evict_select: the rows to keep, kept [B, budget] int32 rising, kept_lens [B] int32, from scores
+        [B, stride] fp32: the first n_sink, the last n_recent and the largest sums between."""
+        import torch
+        _expect("scores", scores, torch.float32, self.B, None)
+        _expect("seq_lens", seq_lens, torch.int32, self.B)
+        _expect("kept", kept, torch.int32, self.B, None)
+        _expect("kept_lens", kept_lens, torch.int32, self.B)
+        _check(self._lib.lca_evict_select(self._h, _ptr(scores), scores.shape[1], _ptr(seq_lens), n_sink, n_recent,
+                                          kept.shape[1], _ptr(kept), _ptr(kept_lens), _stream_handle(stream)),
+               "lca_evict_select")
+
+    def cache_compact(self, c_pool, k_pool, page_size: int, block_table, src, n_src, dst0=None, scores=None,
+                      stream=None) -> None:
+        """lca_cache_compact: row dst0[b] + j of sequence b becomes its row src[b, j], j < n_src[b], in place
+        (with the sums, if given): an eviction's kept rows, or a committed path of drafted tokens."""
+        import torch
+        cache = self._cache_args(c_pool, k_pool, page_size, block_table)
+        _expect("src", src, torch.int32, self.B, None)
+        _expect("n_src", n_src, torch.int32, self.B)
+        if dst0 is not None:
+            _expect("dst0", dst0, torch.int32, self.B)
+        if scores is not None:
+            _expect("scores", scores, torch.float32, self.B, None)
+        _check(self._lib.lca_cache_compact(self._h, *cache, _ptr(src), src.shape[1], _ptr(n_src), _ptr(dst0),
+                                           _ptr(scores), 0 if scores is None else scores.shape[1],
+                                           _stream_handle(stream)), "lca_cache_compact")
+
     def device_error(self, stream=None) -> int:
         return int(self._lib.lca_get_device_error(self._h, _stream_handle(stream)))
 
@@ -284,3 +411,23 @@ def stored_rows(L: int, g: int, w: int) -> int:
 
 def slice_groups(L: int, g: int, w: int, pos0: int, n_tok: int) -> int:
     return int(load_library().lca_slice_groups(L, g, w, pos0, n_tok))
+
+
+def tree_mask(parents):
+    """The mask words of draft trees: parents int [B, T] (a torch tensor, on any device), parents[b, i] < i the
+    parent of node i, -1 where it follows the cached tokens.  Returns int64 [B, T]: bit j of word i says that
+    node j is node i or one of its ancestors."""
+    import torch
+    p = parents.to(torch.int64)
+    B, T = p.shape
+    if T > MAX_DRAFT:
+        raise LcaError(LCA_ERR_INVALID_ARG, f"tree_mask: {T} nodes, at most {MAX_DRAFT}")
+    node = torch.arange(T, device=p.device)
+    if bool(((p < -1) | (p >= node[None, :])).any()):
+        raise LcaError(LCA_ERR_INVALID_ARG, "tree_mask: a parent has to come before its child (or be -1)")
+    words = (torch.ones_like(node) << node).expand(B, T).clone()
+    up = p
+    for _ in range(max(T - 1, 0).bit_length()):      # 1, 2, 4, ... generations at a time
+        words = words | torch.where(up >= 0, torch.gather(words, 1, up.clamp(min=0)), torch.zeros_like(words))
+        up = torch.where(up >= 0, torch.gather(up, 1, up.clamp(min=0)), up)
+    return words

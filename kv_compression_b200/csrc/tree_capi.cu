@@ -1,0 +1,277 @@
+// tree_capi.cu -- the part of include/lca.h for drafted tokens and eviction:
+// tree attention, accumulated attention weights, the choice of the rows to
+// keep and their compaction.  As in lca_capi.cu no exception crosses the ABI,
+// nothing aborts, and argument errors are reported before anything is launched.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "evict_kernel.cuh"
+#include "lca.h"
+#include "plan.cuh"
+#include "tree_common.cuh"
+#include "tree_simt_kernel.cuh"
+
+namespace {
+
+using lca::TreeBatch;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+constexpr size_t kMaxSmem = 232448;
+
+// ---------------------------------------------------------------- workspace
+// [TreeSplit x B][(M, Z) of every slot row][O of every slot row], each part
+// 256-byte aligned.
+struct Workspace {
+  int64_t slot_rows;      // rows of partials
+  size_t mz, o, bytes;    // offsets, and the whole
+};
+
+// Parts the CUDA-core kernel cuts each sequence into: about four CTAs per SM
+// over B and the blocks of 8 rows; one part writes its output itself.
+int64_t simt_parts(const lca_plan* p, int T) {
+  const int64_t units = (int64_t)p->B * ceil_div((int64_t)T * p->H, lca::kTreeSimtRows);
+  return std::max<int64_t>(1, std::min<int64_t>(4LL * p->num_sms / units, ceil_div(p->max_L, lca::kTreeSimtTile)));
+}
+
+Workspace workspace_of(const lca_plan* p, int T) {
+  Workspace w;
+  const int64_t parts = simt_parts(p, T);
+  w.slot_rows = parts > 1 ? parts * p->B * round_up((int64_t)T * p->H, lca::kTreeSimtRows) : 0;
+  w.mz = (size_t)round_up((int64_t)p->B * sizeof(lca::TreeSplit), 256);
+  w.o = w.mz + (size_t)round_up(w.slot_rows * 2 * sizeof(float), 256);
+  w.bytes = w.o + (size_t)w.slot_rows * p->d_c * sizeof(float);
+  return w;
+}
+
+// ---------------------------------------------------------------- argument checks
+lca_status check_plan(const lca_plan* p) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LCA_ERR_CUDA;
+  return dev == p->device ? LCA_OK : LCA_ERR_PLAN_MISMATCH;
+}
+
+// The cache arguments common to the entry points, and their bound on lengths.
+lca_status check_cache(const lca_plan* p, const void* c_pool, const void* k_pool, int64_t num_pages, int page_size,
+                       const int32_t* block_table, int64_t max_pages, TreeBatch* t) {
+  if (!p || !c_pool || !k_pool || num_pages < 1 || page_size < 1 || max_pages < 1) return LCA_ERR_INVALID_ARG;
+  if (block_table ? page_size % 64 != 0 : num_pages < p->B) return LCA_ERR_INVALID_ARG;
+  if ((uint64_t)num_pages > (uint64_t)INT32_MAX / (uint64_t)page_size) return LCA_ERR_UNSUPPORTED;
+  std::memset(t, 0, sizeof(*t));
+  t->c = c_pool;
+  t->k = k_pool;
+  t->num_pages = num_pages;
+  t->page_size = page_size;
+  t->table = block_table;
+  t->max_pages = block_table ? max_pages : 1;
+  t->B = p->B;
+  t->H = p->H;
+  t->d_c = p->d_c;
+  t->d_r = p->d_r;
+  const int64_t rows = t->max_pages > INT32_MAX / page_size ? INT32_MAX : t->max_pages * page_size;
+  t->cap = std::min<int64_t>(std::min<int64_t>(p->max_L, rows), INT32_MAX - 4096);
+  t->err = p->err;
+  return LCA_OK;
+}
+
+lca_status check_batch(const lca_plan* p, int n_draft, const int32_t* seq_lens, const int32_t* draft_lens,
+                       const uint64_t* mask, TreeBatch* t) {
+  if (!seq_lens || n_draft < 1 || n_draft > lca::kTreeMaxDraft) return LCA_ERR_INVALID_ARG;
+  if ((int64_t)p->B * n_draft * p->H > INT32_MAX || p->B > 65535) return LCA_ERR_UNSUPPORTED;
+  if (!aligned(seq_lens, 4) || !aligned(draft_lens, 4) || !aligned(mask, 8) || !aligned(t->table, 4))
+    return LCA_ERR_ALIGNMENT;
+  t->T = n_draft;
+  t->seq_lens = seq_lens;
+  t->draft_lens = draft_lens;
+  t->mask = reinterpret_cast<const unsigned long long*>(mask);
+  return LCA_OK;
+}
+
+template <typename K>
+bool allow_smem(K kernel, size_t smem) {
+  return smem <= 48 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+}
+
+lca_status launched() { return cudaGetLastError() == cudaSuccess ? LCA_OK : LCA_ERR_CUDA; }
+
+// The merge of the parts, a programmatic dependent of the kernel that wrote them.
+template <typename T>
+lca_status launch_merge(const lca::TreeMergeParams& mp, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const int64_t R = (int64_t)mp.t.T * mp.t.H;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(R, 65535), (unsigned)mp.t.B, 1);
+  cfg.blockDim = dim3(lca::kTreeMergeThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lca::lca_tree_merge_kernel<T>, mp) == cudaSuccess ? LCA_OK : LCA_ERR_CUDA;
+}
+
+template <typename T>
+lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c, const void* q_r, void* out,
+                         float* lse, uint8_t* ws, const Workspace& w, cudaStream_t stream) {
+  lca::TreeSimtParams sp = {};
+  sp.t = t;
+  sp.q_c = q_c;
+  sp.q_r = q_r;
+  sp.n_split = (int)simt_parts(p, t.T);
+  sp.split = reinterpret_cast<lca::TreeSplit*>(ws);
+  sp.part_mz = reinterpret_cast<float*>(ws + w.mz);
+  sp.part_o = reinterpret_cast<float*>(ws + w.o);
+  sp.out = out;
+  sp.lse = lse;
+  const size_t smem = lca::tree_simt_smem(t.d_c, t.d_r);
+  if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
+  if (!allow_smem(lca::lca_tree_simt_kernel<T>, smem)) return LCA_ERR_CUDA;
+  const dim3 grid((unsigned)sp.n_split, (unsigned)ceil_div((int64_t)t.T * t.H, lca::kTreeSimtRows), (unsigned)t.B);
+  lca::lca_tree_simt_kernel<T><<<grid, lca::kTreeSimtThreads, smem, stream>>>(sp);
+  const lca_status st = launched();
+  if (st != LCA_OK) return st;
+  lca::TreeMergeParams mp = {};
+  mp.t = t;
+  mp.part_o = sp.part_o;
+  mp.part_mz = sp.part_mz;
+  mp.split = sp.split;
+  mp.rows_per_block = lca::kTreeSimtRows;
+  mp.direct = sp.n_split == 1;
+  mp.out = out;
+  mp.lse = lse;
+  return launch_merge<T>(mp, stream);
+}
+
+template <typename T>
+lca_status run_mass_simt(const lca_plan* p, const lca::MassParams& mp, cudaStream_t stream) {
+  const size_t smem = lca::tree_simt_smem(mp.t.d_c, mp.t.d_r);
+  if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
+  if (!allow_smem(lca::lca_mass_simt_kernel<T>, smem)) return LCA_ERR_CUDA;
+  const int64_t blocks = std::min<int64_t>(ceil_div(mp.t.cap, lca::kTreeSimtTile), std::max<int64_t>(1, 8LL * p->num_sms / p->B));
+  lca::lca_mass_simt_kernel<T><<<dim3((unsigned)blocks, (unsigned)p->B), lca::kTreeSimtThreads, smem, stream>>>(mp);
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lca_tree_workspace(const lca_plan* p, int n_draft) {
+  if (!p || n_draft < 1 || n_draft > lca::kTreeMaxDraft) return -1;
+  return (int64_t)workspace_of(p, n_draft).bytes;
+}
+
+lca_status lca_tree_decode(lca_plan* p, const void* q_c, const void* q_r, int n_draft, const void* c_pool,
+                           const void* k_pool, int64_t num_pages, int page_size, const int32_t* block_table,
+                           int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                           const uint64_t* mask, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  TreeBatch t;
+  lca_status st = check_cache(p, c_pool, k_pool, num_pages, page_size, block_table, max_pages, &t);
+  if (st != LCA_OK) return st;
+  if (!q_c || !q_r || !out || !workspace) return LCA_ERR_INVALID_ARG;
+  if ((st = check_batch(p, n_draft, seq_lens, draft_lens, mask, &t)) != LCA_OK) return st;
+  const Workspace w = workspace_of(p, n_draft);
+  if (workspace_bytes < (int64_t)w.bytes) return LCA_ERR_INVALID_ARG;
+  if (!aligned(q_c, 16) || !aligned(q_r, 16) || !aligned(c_pool, 16) || !aligned(k_pool, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(workspace, 256))
+    return LCA_ERR_ALIGNMENT;
+  if ((st = check_plan(p)) != LCA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (p->kernel_pref > 1) return LCA_ERR_UNSUPPORTED;
+  if (p->dt == LCA_F32) return run_tree_simt<float>(p, t, q_c, q_r, out, lse, ws, w, s);
+  return run_tree_simt<__nv_bfloat16>(p, t, q_c, q_r, out, lse, ws, w, s);
+}
+
+lca_status lca_attn_mass(lca_plan* p, const void* q_c, const void* q_r, int n_draft, const void* c_pool,
+                         const void* k_pool, int64_t num_pages, int page_size, const int32_t* block_table,
+                         int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* mask,
+                         const float* lse, const float* prev, float decay, float* scores, int64_t score_stride,
+                         void* workspace, int64_t workspace_bytes, void* stream) {
+  lca::MassParams mp = {};
+  lca_status st = check_cache(p, c_pool, k_pool, num_pages, page_size, block_table, max_pages, &mp.t);
+  if (st != LCA_OK) return st;
+  if (!q_c || !q_r || !lse || !scores || !workspace || score_stride < 1) return LCA_ERR_INVALID_ARG;
+  if ((st = check_batch(p, n_draft, seq_lens, draft_lens, mask, &mp.t)) != LCA_OK) return st;
+  const Workspace w = workspace_of(p, n_draft);
+  if (workspace_bytes < (int64_t)w.bytes) return LCA_ERR_INVALID_ARG;
+  if (!aligned(q_c, 16) || !aligned(q_r, 16) || !aligned(c_pool, 16) || !aligned(k_pool, 16) || !aligned(lse, 4) ||
+      !aligned(prev, 4) || !aligned(scores, 4) || !aligned(workspace, 256))
+    return LCA_ERR_ALIGNMENT;
+  if ((st = check_plan(p)) != LCA_OK) return st;
+  mp.t.cap = std::min(mp.t.cap, score_stride);
+  mp.q_c = q_c;
+  mp.q_r = q_r;
+  mp.lse = lse;
+  mp.prev = prev;
+  mp.scores = scores;
+  mp.stride = score_stride;
+  mp.decay = decay;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p->kernel_pref > 1) return LCA_ERR_UNSUPPORTED;
+  return p->dt == LCA_F32 ? run_mass_simt<float>(p, mp, s) : run_mass_simt<__nv_bfloat16>(p, mp, s);
+}
+
+lca_status lca_evict_select(lca_plan* p, const float* scores, int64_t score_stride, const int32_t* seq_lens,
+                            int64_t n_sink, int64_t n_recent, int64_t budget, int32_t* kept, int32_t* kept_lens,
+                            void* stream) {
+  if (!p || !scores || !seq_lens || !kept || !kept_lens || score_stride < 1 || n_sink < 0 || n_recent < 0 ||
+      budget < 1 || budget > INT32_MAX || n_sink > budget || n_recent > budget - n_sink)
+    return LCA_ERR_INVALID_ARG;
+  if (!aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
+    return LCA_ERR_ALIGNMENT;
+  const lca_status st = check_plan(p);
+  if (st != LCA_OK) return st;
+  lca::SelectParams sp = {};
+  sp.scores = scores;
+  sp.stride = score_stride;
+  sp.seq_lens = seq_lens;
+  sp.B = p->B;
+  sp.cap = std::min<int64_t>(std::min<int64_t>(p->max_L, score_stride), INT32_MAX - 4096);
+  sp.n_sink = (int)n_sink;
+  sp.n_recent = (int)n_recent;
+  sp.budget = (int)budget;
+  sp.kept = kept;
+  sp.kept_lens = kept_lens;
+  sp.err = p->err;
+  lca::lca_select_kernel<<<p->B, lca::kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(sp);
+  return launched();
+}
+
+lca_status lca_cache_compact(lca_plan* p, void* c_pool, void* k_pool, int64_t num_pages, int page_size,
+                             const int32_t* block_table, int64_t max_pages, const int32_t* src, int64_t src_stride,
+                             const int32_t* n_src, const int32_t* dst0, float* scores, int64_t score_stride,
+                             void* stream) {
+  lca::CompactParams cp = {};
+  lca_status st = check_cache(p, c_pool, k_pool, num_pages, page_size, block_table, max_pages, &cp.t);
+  if (st != LCA_OK) return st;
+  if (!src || !n_src || src_stride < 1 || src_stride > INT32_MAX || (scores && score_stride < 1)) return LCA_ERR_INVALID_ARG;
+  if (p->B > 65535) return LCA_ERR_UNSUPPORTED;
+  if (!aligned(c_pool, 16) || !aligned(k_pool, 16) || !aligned(block_table, 4) || !aligned(src, 4) ||
+      !aligned(n_src, 4) || !aligned(dst0, 4) || !aligned(scores, 4))
+    return LCA_ERR_ALIGNMENT;
+  if ((st = check_plan(p)) != LCA_OK) return st;
+  if (scores) cp.t.cap = std::min(cp.t.cap, score_stride);
+  cp.elem = p->dt == LCA_F32 ? 4 : 2;
+  cp.src = src;
+  cp.src_stride = src_stride;
+  cp.n_src = n_src;
+  cp.dst0 = dst0;
+  cp.scores = scores;
+  cp.score_stride = score_stride;
+  cp.strip = 8;
+  cp.strips_c = (int)ceil_div((int64_t)p->d_c * cp.elem / 16, cp.strip);
+  cp.strips_k = (int)ceil_div((int64_t)p->d_r * cp.elem / 16, cp.strip);
+  const dim3 grid((unsigned)(cp.strips_c + cp.strips_k + (scores ? 1 : 0)), (unsigned)p->B);
+  lca::lca_compact_kernel<<<grid, lca::kCompactThreads, 0, static_cast<cudaStream_t>(stream)>>>(cp);
+  return launched();
+}
+
+}  // extern "C"
