@@ -16,9 +16,9 @@ LIB_CHECKED = os.path.join(HERE, "liblca_checked.so")
 SOURCES = {
     "lca_capi.cu": ["checks.cuh", "device_input.cuh", "plan.cuh", "ptx.cuh", "tc_kernel.cuh", "pair_kernel.cuh",
                     "simt_kernel.cuh", "combine_kernel.cuh", "condense_kernel.cuh", "paged_kernel.cuh",
-                    "gqa_kernel.cuh"],
+                    "gqa_kernel.cuh", "tmap.cuh"],
     "tree_capi.cu": ["checks.cuh", "device_input.cuh", "plan.cuh", "ptx.cuh", "tree_common.cuh",
-                     "tree_simt_kernel.cuh", "evict_kernel.cuh"],
+                     "tree_simt_kernel.cuh", "tree_schedule.cuh", "tree_tc_kernel.cuh", "evict_kernel.cuh", "tmap.cuh"],
 }
 HEADERS = sorted({h for hs in SOURCES.values() for h in hs})
 

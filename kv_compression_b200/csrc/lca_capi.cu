@@ -21,6 +21,7 @@
 #include "plan.cuh"
 #include "simt_kernel.cuh"
 #include "tc_kernel.cuh"
+#include "tmap.cuh"
 
 // Fixed device scratch of lca_decode_noalloc (zero at module load): split
 // partials [slots][H][d_c] and [slots][H][2] floats, then the device error
@@ -34,6 +35,8 @@ constexpr size_t kNoAllocErrOffset = kNoAllocOFloats + kNoAllocMzFloats;
 static __device__ __align__(256) float lca_noalloc_scratch[kNoAllocErrOffset + 64];
 
 namespace {
+
+using lca::make_map;
 
 constexpr int64_t kDefaultTimeoutNs = 2000000000LL;  // 2 s bound on any in-kernel wait
 
@@ -49,39 +52,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int simt_target_splits(const lca_plan* p) {
   const int64_t bh = (int64_t)p->B * p->H;
   return (int)std::max<int64_t>(1, ceil_div(2LL * p->num_sms, bh));
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  }
-  return fn;
-}
-
-// bf16 matrix [rows][inner], box [box_rows][64], 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t gdim[2] = {inner, rows};
-  const cuuint64_t gstride[1] = {inner * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estride[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), gdim, gstride, box,
-            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 enum Kernel { kNone = 0, kSimt = 1, kTc = 2, kPair = 3 };

@@ -13,7 +13,9 @@
 #include "lca.h"
 #include "plan.cuh"
 #include "tree_common.cuh"
+#include "tmap.cuh"
 #include "tree_simt_kernel.cuh"
+#include "tree_tc_kernel.cuh"
 
 namespace {
 
@@ -40,10 +42,20 @@ int64_t simt_parts(const lca_plan* p, int T) {
   return std::max<int64_t>(1, std::min<int64_t>(4LL * p->num_sms / units, ceil_div(p->max_L, lca::kTreeSimtTile)));
 }
 
+// The tensor-core kernels' shape.
+bool tc_ok(const lca_plan* p) { return p->dt == LCA_BF16 && p->d_c == lca::ttc::kDC && p->d_r == lca::ttc::kDR; }
+
+// Query rows of a unit: the least of 16, 32, 64 that holds a sequence's rows, 64 where none does.
+int tc_rows(const lca_plan* p, int T) {
+  const int64_t r = (int64_t)T * p->H;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+}
+
 Workspace workspace_of(const lca_plan* p, int T) {
   Workspace w;
   const int64_t parts = simt_parts(p, T);
   w.slot_rows = parts > 1 ? parts * p->B * round_up((int64_t)T * p->H, lca::kTreeSimtRows) : 0;
+  if (tc_ok(p)) w.slot_rows = std::max<int64_t>(w.slot_rows, (int64_t)lca::kTreeMaxWaves * p->num_sms * tc_rows(p, T));
   w.mz = (size_t)round_up((int64_t)p->B * sizeof(lca::TreeSplit), 256);
   w.o = w.mz + (size_t)round_up(w.slot_rows * 2 * sizeof(float), 256);
   w.bytes = w.o + (size_t)w.slot_rows * p->d_c * sizeof(float);
@@ -148,6 +160,50 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   return launch_merge<T>(mp, stream);
 }
 
+template <int N>
+lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, const void* q_r, void* out, float* lse,
+                       uint8_t* ws, const Workspace& w, cudaStream_t stream) {
+  namespace ttc = lca::ttc;
+  ttc::Params tp;
+  std::memset(&tp, 0, sizeof(tp));
+  const uint64_t rows = (uint64_t)t.num_pages * (uint64_t)t.page_size, qrows = (uint64_t)t.B * t.T * t.H;
+  if (!lca::make_map(&tp.tm_c, t.c, ttc::kDC, rows, 64) || !lca::make_map(&tp.tm_k, t.k, ttc::kDR, rows, 64) ||
+      !lca::make_map(&tp.tm_qc, q_c, ttc::kDC, qrows, N) || !lca::make_map(&tp.tm_qr, q_r, ttc::kDR, qrows, N))
+    return LCA_ERR_CUDA;
+  tp.t = t;
+  tp.G = p->num_ctas > 0 ? p->num_ctas : p->num_sms;
+  tp.split = reinterpret_cast<lca::TreeSplit*>(ws);
+  tp.part_mz = reinterpret_cast<float*>(ws + w.mz);
+  tp.part_o = reinterpret_cast<float*>(ws + w.o);
+  tp.slots = w.slot_rows / N;
+  tp.out = static_cast<__nv_bfloat16*>(out);
+  tp.lse = lse;
+  tp.timeout_ns = p->timeout_ns;
+  tp.debug_skip_load = p->debug_skip_load;
+  if (!allow_smem(ttc::lca_tree_tc_kernel<N>, ttc::Layout<N>::kAlloc)) return LCA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)tp.G, 1, 1);
+  cfg.blockDim = dim3(ttc::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = ttc::Layout<N>::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, ttc::lca_tree_tc_kernel<N>, tp) != cudaSuccess) return LCA_ERR_CUDA;
+  lca::TreeMergeParams mp = {};
+  mp.t = t;
+  mp.part_o = tp.part_o;
+  mp.part_mz = tp.part_mz;
+  mp.split = tp.split;
+  mp.rows_per_block = N;
+  mp.direct = true;
+  mp.out = out;
+  mp.lse = lse;
+  return launch_merge<__nv_bfloat16>(mp, stream);
+}
+
 template <typename T>
 lca_status run_mass_simt(const lca_plan* p, const lca::MassParams& mp, cudaStream_t stream) {
   const size_t smem = lca::tree_simt_smem(mp.t.d_c, mp.t.d_r);
@@ -185,7 +241,15 @@ lca_status lca_tree_decode(lca_plan* p, const void* q_c, const void* q_r, int n_
   if ((st = check_plan(p)) != LCA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (p->kernel_pref > 1) return LCA_ERR_UNSUPPORTED;
+  const int pref = p->force_simt ? 1 : p->kernel_pref;      // 1 CUDA-core, 2 tcgen05
+  if (pref > 2 || (pref == 2 && !tc_ok(p))) return LCA_ERR_UNSUPPORTED;
+  if (tc_ok(p) && pref != 1) {
+    switch (tc_rows(p, n_draft)) {
+      case 16: return run_tree_tc<16>(p, t, q_c, q_r, out, lse, ws, w, s);
+      case 32: return run_tree_tc<32>(p, t, q_c, q_r, out, lse, ws, w, s);
+      default: return run_tree_tc<64>(p, t, q_c, q_r, out, lse, ws, w, s);
+    }
+  }
   if (p->dt == LCA_F32) return run_tree_simt<float>(p, t, q_c, q_r, out, lse, ws, w, s);
   return run_tree_simt<__nv_bfloat16>(p, t, q_c, q_r, out, lse, ws, w, s);
 }

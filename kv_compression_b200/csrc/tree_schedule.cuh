@@ -1,0 +1,132 @@
+// tree_schedule.cuh -- how a ragged batch of draft trees is cut into work for
+// CTAs.  Plain arithmetic, written once for a warp (its lanes share the
+// sequences) and for one thread of the host (tests).
+//
+// Sequence b has rb_b blocks of N query rows and tiles_b tiles of 128 tokens.
+// Its tokens are cut into parts_b = ceil(tiles_b / S) parts of nearly equal
+// length (S tiles at most), and a unit is (sequence, part, row block), row
+// blocks fastest: units that read the same tokens run next to each other, so
+// that a tile comes from HBM once and from L2 for the other row blocks.  Unit u
+// goes to CTA u mod G, and its partial to slot u.
+//
+// S is chosen for the time of the longest CTA: k units one after another take
+// about k (S + c) tile times, c for a unit's fixed costs (query block, pipeline
+// fill, partial or output).  For each k up to kTreeMaxWaves the least S with
+// units(S) <= k G is found and the best k taken; where even unsplit sequences
+// make more units than that, none is split (and no slot is used).
+#pragma once
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define LCA_HD __host__ __device__ __forceinline__
+#else
+#define LCA_HD inline
+#endif
+
+namespace lca {
+
+constexpr int kTreeTile = 128;        // tokens
+constexpr int kTreeMaxWaves = 4;
+constexpr int kTreeUnitCost = 2;      // c, in tile times
+
+struct TreeWork {                     // one sequence's
+  int rb, tiles;
+};
+
+LCA_HD TreeWork tree_work(int n, int d, int H, int N) {
+  TreeWork w;
+  w.rb = (d * H + N - 1) / N;
+  w.tiles = d > 0 ? (int)(((int64_t)n + d + kTreeTile - 1) / kTreeTile) : 0;
+  return w;
+}
+
+struct TreeUnit {
+  int b;                              // -1: there is no such unit
+  int rb, part, parts;
+  int t0, t1;                         // tiles
+};
+
+// First tile of part `part` of `parts` over `tiles`.
+LCA_HD int tree_cut(int tiles, int part, int parts) { return (int)((int64_t)tiles * part / parts); }
+
+// Units for parts of at most S tiles.  Lanes: lane() of count(), sum(), scan() (inclusive), first() (the lowest
+// lane where true, -1: none), get() (a lane's value).
+template <class Lanes, class Seq>
+LCA_HD int64_t tree_units(const Lanes& w, const Seq& seq, int B, int S) {
+  int64_t c = 0;
+  for (int b = w.lane(); b < B; b += w.count()) {
+    const TreeWork k = seq(b);
+    c += (int64_t)k.rb * ((k.tiles + S - 1) / S);
+  }
+  return w.sum(c);
+}
+
+// The least S in [1, most] with units(S) <= limit; most + 1 if there is none.
+template <class Lanes, class Seq>
+LCA_HD int tree_least(const Lanes& w, const Seq& seq, int B, int most, int64_t limit) {
+  if (tree_units(w, seq, B, most) > limit) return most + 1;
+  int lo = 1, hi = most;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (tree_units(w, seq, B, mid) <= limit) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// The cost of k waves with their least S (INT64_MAX: not possible).
+LCA_HD int64_t tree_cost(int k, int S, int most) {
+  return S > most ? INT64_MAX : (int64_t)k * (S + kTreeUnitCost);
+}
+
+// Unit u.
+template <class Lanes, class Seq>
+LCA_HD TreeUnit tree_unit(const Lanes& w, const Seq& seq, int B, int S, int64_t u) {
+  int64_t base = 0;
+  for (int b0 = 0; b0 < B; b0 += w.count()) {
+    const int b = b0 + w.lane();
+    TreeWork k = {0, 0};
+    if (b < B) k = seq(b);
+    const int parts = (k.tiles + S - 1) / S;
+    const int64_t incl = base + w.scan((int64_t)k.rb * parts);
+    const int at = w.first(incl > u);
+    if (at >= 0) {
+      TreeUnit r;
+      r.b = b0 + at;
+      const int rb = w.get(k.rb, at), tiles = w.get(k.tiles, at);
+      r.parts = w.get(parts, at);
+      const int i = (int)(u - (w.get(incl, at) - (int64_t)rb * r.parts));
+      r.part = i / rb;
+      r.rb = i - r.part * rb;
+      r.t0 = tree_cut(tiles, r.part, r.parts);
+      r.t1 = tree_cut(tiles, r.part + 1, r.parts);
+      return r;
+    }
+    base = w.get(incl, w.count() - 1);
+  }
+  return TreeUnit{-1, 0, 0, 0, 0, 0};
+}
+
+#ifdef __CUDACC__
+struct WarpLanes {
+  __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
+  __device__ __forceinline__ int count() const { return 32; }
+  __device__ __forceinline__ int64_t sum(int64_t v) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ int64_t scan(int64_t v) const {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane() >= o) v += x;
+    }
+    return v;
+  }
+  __device__ __forceinline__ int first(bool p) const { return __ffs(__ballot_sync(0xffffffffu, p)) - 1; }
+  __device__ __forceinline__ int get(int v, int from) const { return __shfl_sync(0xffffffffu, v, from); }
+  __device__ __forceinline__ int64_t get(int64_t v, int from) const { return __shfl_sync(0xffffffffu, v, from); }
+};
+#endif
+
+}  // namespace lca

@@ -1,0 +1,582 @@
+// tree_tc_kernel.cuh -- draft-tree attention over the latent cache with tcgen05
+// tensor cores (bf16, d_c = 512, d_r = 64).
+//
+// One unit of work is a block of N query rows (node, head) of a sequence and a
+// run of 128-token tiles (tree_schedule.cuh).  Per tile
+//   S^T[128 tokens x N rows] = [C | K]_tile . [q_c | q_r]^T     36 MMAs, M = 128, K = 16
+//   P^T = 2^{S^T log2 e - M}                                    softmax warps, a token a thread
+//   O^T[512 x N] += C_tile^T . P^T                              32 MMAs, in TMEM
+// Tokens are the M side of both products, so the same shared-memory tile is
+// the A operand twice: K-major for S, MN-major (its transpose) for O.  A token
+// is one thread's: its running sums stay in that thread until the unit ends.
+//
+// Why this orientation and N = 64.  An M = 128 MMA of K = 16 takes max(44.7,
+// 32 + N / 4 cycles for its operands' shared-memory reads) (measured: N = 16, 32:
+// 44.7; 64: 48; 128: 64), so N = 64 gives 3264 cycles for 64 x 128 x 1088 MACs
+// (67% of the peak of 64 cycles at N = 128).  With rows on the M side a CTA
+// would need 128 rows x 512 dims of fp32 for O, all of TMEM, or a cluster that
+// exchanges S or P for every tile; O^T of 64 rows takes 256 columns and no
+// exchange.
+//
+// Shared memory: for N = 64 four 32 KB slots hold one tile's C (a slot: 128
+// dims), 16 KB its K, and Q the rest, so a tile is resident once and the next
+// one streams into the slots as O's MMAs release them, slot by slot; P takes
+// K's place, which is read by then.  N <= 32 has a fifth slot and P its own.
+//
+// The reference M of a row rises only when a logit exceeds it by more than 2^8
+// (then Z and O^T are scaled): one barrier with an OR over the softmax warps
+// per tile decides that.
+//
+// Tokens a row does not see get weight 0; because 0 x NaN is not 0, rows of
+// the tile that hold no token are zeroed in shared memory, and a drafted row
+// with an infinity or NaN is zeroed too and makes the sums of the rows that see
+// it NaN.
+//
+// Roles (320 threads): warp 0 loads, warp 1 issues the MMAs, warps 2-9 the
+// softmax (two per TMEM lane quarter, each with half of the rows).  Every wait
+// is bounded: when one runs out the CTA records it, lets its copies and MMAs
+// land, frees TMEM and exits.
+#pragma once
+#include <cuda.h>
+
+#include "checks.cuh"
+#include "ptx.cuh"
+#include "tree_common.cuh"
+#include "tree_schedule.cuh"
+
+namespace lca {
+namespace ttc {
+
+constexpr int kDC = 512, kDR = 64;
+constexpr int kChunk = 128 * 128;           // [128 tokens][64 bf16], 128-byte swizzle
+constexpr int kSlot = 2 * kChunk;           // 128 latent dims of a tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (2 + kSoftmaxWarps);
+constexpr int kMaxSlots = 5;
+constexpr int kBarSoftmax = 1;              // named barrier of the softmax warps
+constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
+constexpr float kRaise = 8.f;
+constexpr int kErrTimeout = 1;
+constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
+
+template <int N>
+struct Layout {
+  static constexpr bool kAlias = N == 64;              // P in K's place
+  static constexpr int kSlots = N == 64 ? 4 : 5;
+  static constexpr int kQChunk = N * 128;
+  static constexpr int kOffK = kSlots * kSlot;
+  static constexpr int kOffQ = kOffK + kChunk;
+  static constexpr int kOffP = kAlias ? kOffK : kOffQ + 9 * kQChunk;
+  static constexpr int kOffWord = kOffQ + 9 * kQChunk + (kAlias ? 0 : 128 * N * 2);   // mask words of the rows
+  static constexpr int kOffRed = kOffWord + 8 * N;     // float [4][N]
+  static constexpr int kOffM = kOffRed + 16 * N;       // float2 [N]: the rows' (M, Z)
+  static constexpr int kOffBar = kOffM + 8 * N;
+  static constexpr int kBars = 2 * kMaxSlots + 8;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S; nodes with a broken row
+  static constexpr int kBytes = kOffMisc + 32;
+  static constexpr int kAlloc = kBytes + 1024;         // slack for the 1 KB alignment
+  static_assert(kAlloc <= 232448, "shared memory of one CTA");
+};
+
+struct Params {
+  CUtensorMap tm_c, tm_k;       // pools, box [64 rows][64]
+  CUtensorMap tm_qc, tm_qr;     // queries as [B T H rows][..], box [N rows][64]
+  TreeBatch t;
+  int G;                        // CTAs
+  float* part_o;                // [slots][N][512]
+  float* part_mz;               // [slots][N][2]
+  TreeSplit* split;
+  int64_t slots;
+  __nv_bfloat16* out;
+  float* lse;
+  uint64_t timeout_ns;
+  int debug_skip_load;
+};
+
+struct Wait {
+  volatile int* abort;
+  int* err;
+  uint64_t timeout_ns;
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, const Wait& w, int where, bool honour) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t spin = 1;; ++spin) {
+    if (ptx::mbar_try_wait_sleep(bar, parity, 100)) return true;
+    if (honour && *w.abort) return false;
+    if ((spin & 7u) == 0 && ptx::globaltimer_ns() - t0 > w.timeout_ns) {
+      *w.abort = 1;
+      if (atomicOr(w.err, kErrTimeout) == 0) atomicExch(w.err + 1, where);
+      return false;
+    }
+  }
+}
+// A bounded wait of one thread; `warp_wait` the same for a whole warp, which leaves it together.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Wait& w, int where, bool honour = true) {
+  return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity, w, where, honour);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Wait& w, int where) {
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (!ok) ok = wait_slow(bar, parity, w, where, true);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int C>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[C]) {
+  if constexpr (C == 32) ptx::tmem_ld32(addr, v);
+  else if constexpr (C == 16) ptx::tmem_ld16(addr, v);
+  else ptx::tmem_ld8(addr, v);
+}
+// True if one of the 8 bf16 in `u` is an infinity or NaN.
+__device__ __forceinline__ bool any_nonfinite(uint4 u) {
+  auto bad = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+  return bad(u.x) || bad(u.y) || bad(u.z) || bad(u.w);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_constant__ Params p) {
+  using L = Layout<N>;
+  constexpr int kSlots = L::kSlots;
+  constexpr int kKAt = L::kAlias ? 4 : 1;   // K is taken before this column slot of the tile (last where P waits for it)
+  constexpr int C = N / 2;                  // rows of a softmax thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t *full = bars, *empty = bars + kMaxSlots, *k_full = bars + 2 * kMaxSlots, *k_empty = k_full + 1,
+           *q_full = k_full + 2, *q_empty = k_full + 3, *s_full = k_full + 4, *p_full = k_full + 5,
+           *o_full = k_full + 6, *drain = k_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  int* s_least = reinterpret_cast<int*>(smem + L::kOffMisc + 8);       // [kTreeMaxWaves]
+  unsigned long long* broken = reinterpret_cast<unsigned long long*>(smem + L::kOffMisc + 24);
+  const TreeBatch& t = p.t;
+  const Wait wt = {abort_flag, t.err, p.timeout_ns};
+  const WarpLanes lanes;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(full + i, 1);
+      ptx::mbar_init(empty + i, 1);
+    }
+    ptx::mbar_init(k_full, 1);
+    ptx::mbar_init(k_empty, 1);
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(p_full, kSoftmaxWarps);
+    ptx::mbar_init(o_full, 1);
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    *broken = 0ull;
+    ptx::fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&p.tm_c);
+    ptx::prefetch_tmap(&p.tm_k);
+    ptx::prefetch_tmap(&p.tm_qc);
+    ptx::prefetch_tmap(&p.tm_qr);
+  }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  // ---- the cut: one warp per number of waves
+  auto seq = [&](int b) {
+    const TreeLens l = tree_lens(t, b);
+    return tree_work(l.n, l.d, t.H, N);
+  };
+  int most = 1;
+  for (int b = lane; b < t.B; b += 32) most = max(most, seq(b).tiles);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (warp >= 2 && warp < 2 + kTreeMaxWaves) {
+    const int k = warp - 1;
+    const int S = tree_least(lanes, seq, t.B, most, (int64_t)k * p.G);
+    if (lane == 0) s_least[k - 1] = S;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int S = most;
+  int64_t best = INT64_MAX;
+#pragma unroll
+  for (int k = 1; k <= kTreeMaxWaves; ++k) {
+    const int64_t c = tree_cost(k, s_least[k - 1], most);
+    if (c < best) {
+      best = c;
+      S = s_least[k - 1];
+    }
+  }
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    int64_t np = 0;             // slots filled
+    int nk = 0, nq = 0;         // K tiles, query blocks
+    int64_t sent[kMaxSlots];    // loads into each slot (for the last wait)
+#pragma unroll
+    for (int i = 0; i < kMaxSlots; ++i) sent[i] = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok; u += p.G) {
+      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+      if (un.b < 0) break;
+      if (lane == 0) {
+        const TreeLens l = tree_lens(t, un.b);
+        const int total = l.n + l.d;
+        const int qrow = (int)((int64_t)un.b * t.T * t.H + (int64_t)un.rb * N);
+        if (nq > 0) ok = wait(q_empty, (nq - 1) & 1, wt, 0xC10);
+        if (ok) {
+          ptx::mbar_arrive_expect_tx(q_full, 9 * L::kQChunk);
+          for (int c = 0; c < 8; ++c) ptx::tma_load_2d(smem + L::kOffQ + c * L::kQChunk, &p.tm_qc, 64 * c, qrow, q_full);
+          ptx::tma_load_2d(smem + L::kOffQ + 8 * L::kQChunk, &p.tm_qr, 0, qrow, q_full);
+          ++nq;
+        }
+        for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
+          const int pos = tile * kTreeTile;
+          const int r0 = (int)tree_row(t, un.b, pos, 0xB05);
+          // a second half without tokens is loaded from the first half's rows, and zeroed later
+          const int r1 = pos + 64 < total ? (int)tree_row(t, un.b, pos + 64, 0xB05) : r0;
+          for (int i = 0; i < 5 && ok; ++i) {
+            if (i == kKAt) {
+              if (nk > 0) ok = wait(k_empty, (nk - 1) & 1, wt, 0xC11);
+              if (!ok) break;
+              ptx::mbar_arrive_expect_tx(k_full, kChunk);
+              ptx::tma_load_2d(smem + L::kOffK, &p.tm_k, 0, r0, k_full);
+              ptx::tma_load_2d(smem + L::kOffK + kChunk / 2, &p.tm_k, 0, r1, k_full);
+              ++nk;
+              continue;
+            }
+            const int m = i < kKAt ? i : i - 1;
+            const int slot = (int)(np % kSlots);
+            const int64_t use = np / kSlots;
+            if (use > 0) ok = wait(empty + slot, (uint32_t)(use - 1) & 1, wt, 0xC12);
+            if (!ok) break;
+            if (!(p.debug_skip_load && np == 0)) {
+              ptx::mbar_arrive_expect_tx(full + slot, kSlot);
+              uint8_t* dst = smem + slot * kSlot;
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch) {
+                ptx::tma_load_2d(dst + ch * kChunk, &p.tm_c, 128 * m + 64 * ch, r0, full + slot);
+                ptx::tma_load_2d(dst + ch * kChunk + kChunk / 2, &p.tm_c, 128 * m + 64 * ch, r1, full + slot);
+              }
+#pragma unroll
+              for (int q = 0; q < kMaxSlots; ++q)
+                if (q == slot) sent[q] = use + 1;
+            }
+            ++np;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {            // every copy lands before the CTA may exit
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (sent[i] > 0) wait(full + i, (uint32_t)(sent[i] - 1) & 1, wt, 0xC1F, false);
+      if (nk > 0) wait(k_full, (nk - 1) & 1, wt, 0xC1F, false);
+      if (nq > 0) wait(q_full, (nq - 1) & 1, wt, 0xC1F, false);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, N, 0, 0);     // both K-major
+    constexpr uint32_t kIdO = ptx::idesc_bf16_f32(128, N, 1, 1);     // both MN-major
+    const uint64_t d_c = ptx::smem_desc(ptx::smem_u32(smem), 16, 1024, ptx::kSwizzle128B);
+    const uint64_t d_k = ptx::smem_desc(ptx::smem_u32(smem + L::kOffK), 16, 1024, ptx::kSwizzle128B);
+    const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(smem + L::kOffQ), 16, 1024, ptx::kSwizzle128B);
+    const uint64_t d_ct = ptx::smem_desc(ptx::smem_u32(smem), kChunk, 1024, ptx::kSwizzle128B);
+    const uint64_t d_p = ptx::smem_desc(ptx::smem_u32(smem + L::kOffP), 128, 2048, ptx::kSwizzleNone);
+    int64_t np = 0;
+    int it = 0, nq = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok; u += p.G) {
+      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+      if (un.b < 0) break;
+      if (lane == 0) {
+        ok = wait(q_full, nq & 1, wt, 0xC20);
+        ++nq;
+        for (int tile = un.t0; tile < un.t1 && ok; ++tile, ++it) {
+          bool acc = false;
+          for (int i = 0; i < 5 && ok; ++i) {
+            if (i == kKAt) {
+              ok = wait(k_full, it & 1, wt, 0xC21);
+              if (!ok) break;
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ptx::mma_bf16_ss(tmem + kColS, d_k + (uint64_t)((32 * k) >> 4),
+                                 d_q + (uint64_t)((8 * L::kQChunk + 32 * k) >> 4), kIdS, acc);
+                acc = true;
+              }
+              if (!L::kAlias) ptx::mma_commit(k_empty);
+              continue;
+            }
+            const int m = i < kKAt ? i : i - 1;
+            const int slot = (int)((np + m) % kSlots);
+            ok = wait(full + slot, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC22);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ptx::mma_bf16_ss(tmem + kColS, d_c + (uint64_t)((slot * kSlot + ch * kChunk + 32 * k) >> 4),
+                                 d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, acc);
+                acc = true;
+              }
+          }
+          if (!ok) break;
+          ptx::mma_commit(s_full);
+          if (tile + 1 == un.t1) ptx::mma_commit(q_empty);
+          ok = wait(p_full, it & 1, wt, 0xC23);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t first = tile > un.t0 ? 1u : 0u;
+          for (int m = 0; m < 4; ++m) {
+            const int slot = (int)((np + m) % kSlots);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              ptx::mma_bf16_ss(tmem + kColO + N * m, d_ct + (uint64_t)((slot * kSlot + 2048 * k) >> 4),
+                               d_p + (uint64_t)((256 * k) >> 4), kIdO, k > 0 ? 1u : first);
+            ptx::mma_commit(empty + slot);
+          }
+          if (L::kAlias) ptx::mma_commit(k_empty);
+          if (tile + 1 == un.t1) ptx::mma_commit(o_full);
+          np += 4;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {            // and every MMA
+      ptx::mma_commit(drain);
+      wait(drain, 0, wt, 0xC2F, false);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int sw = warp - 2;
+    const int quarter = warp & 3, half = sw >> 2;     // TMEM lanes 32 quarter .., rows C half ..
+    const int tok = 32 * quarter + lane;              // this thread's token of a tile
+    const int sid = tid - 64;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + C * half;
+    unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord);
+    float* red = reinterpret_cast<float*>(smem + L::kOffRed);
+    float2* row_mz = reinterpret_cast<float2*>(smem + L::kOffM);
+    uint8_t* pt = smem + L::kOffP + (C / 8) * half * 2048 + tok * 16;
+    int64_t np = 0;
+    int it = 0, nu = 0;
+    bool ok = true;
+    // the sequences' records for the merge, by the first CTA
+    if (blockIdx.x == 0 && sw == 7) {
+      int64_t base = 0;
+      for (int b0 = 0; b0 < t.B; b0 += 32) {
+        const int b = b0 + lane;
+        TreeWork k = {0, 0};
+        bool bad = false;
+        if (b < t.B) {
+          k = seq(b);
+          bad = tree_lens(t, b).bad;
+        }
+        const int parts = (k.tiles + S - 1) / S;
+        const int64_t mine = (int64_t)k.rb * parts, incl = base + lanes.scan(mine);
+        if (b < t.B) p.split[b] = TreeSplit{(int)(incl - mine), parts, k.rb, bad ? 1 : 0};
+        if (bad) input_error(t.err, 0xB01);
+        base = lanes.get(incl, 31);
+      }
+    }
+    for (int64_t u = blockIdx.x; ok; u += p.G, ++nu) {
+      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+      if (un.b < 0) break;
+      const TreeLens l = tree_lens(t, un.b);
+      const int total = l.n + l.d;
+      const int rows = min(N, l.d * t.H - un.rb * N);
+      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);    // the last unit's words and sums are read
+      if (sid < N) words[sid] = sid < rows ? tree_word(t, un.b, (un.rb * N + sid) / t.H) : 0ull;
+      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      float M[C], Z[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        M[c] = kEmpty;
+        Z[c] = 0.f;
+      }
+      for (int tile = un.t0; tile < un.t1; ++tile, ++it, np += 4) {
+        const int pos0 = tile * kTreeTile;
+        bool live = warp_wait(s_full, it & 1, wt, 0xC30);
+        ptx::tc_fence_after();
+        float x[C];
+        tmem_load<C>(lane_base + kColS, x);
+        ptx::tmem_wait_ld();
+        const bool special = pos0 + kTreeTile > l.n;           // drafted tokens, or the end, in this tile
+        uint32_t hurt = 0;                                     // rows that see this thread's broken token
+        if (special) {
+          // zero what is no token, and drafted rows that hold an infinity or NaN
+          for (int m = 0; m < 4; ++m)
+            live = warp_wait(full + (np + m) % kSlots, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC31) && live;
+          for (int r = sw; r < kTreeTile; r += kSoftmaxWarps) {
+            const int pos = pos0 + r;
+            if (pos < l.n) continue;
+            uint4* at[2];
+            bool bad = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {                      // 8 chunks of 128 bytes, 16 a lane
+              const int ch = 4 * h + (lane >> 3);
+              at[h] = reinterpret_cast<uint4*>(smem + ((np + (ch >> 1)) % kSlots) * kSlot + (ch & 1) * kChunk + r * 128) + (lane & 7);
+              bad = bad || any_nonfinite(*at[h]);
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (bad || pos >= total) {
+              *at[0] = make_uint4(0, 0, 0, 0);
+              *at[1] = make_uint4(0, 0, 0, 0);
+            }
+            if (bad && pos < total && lane == 0) atomicOr(broken, 1ull << (pos - l.n));
+          }
+          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+          const int node = pos0 + tok - l.n;
+          if (node >= 0) {
+            const bool in = node < l.d;
+            const bool bk = in && ((*broken >> node) & 1ull);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              const bool sees = in && ((words[C * half + c] >> node) & 1ull);
+              if (sees && bk) hurt |= 1u << c;
+              if (!sees || bk) x[c] = -INFINITY;
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          x[c] = x[c] * kTreeLog2e;
+          top = fmaxf(top, x[c] - M[c]);
+        }
+        if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, top > kRaise || !live)) {
+          if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, !live)) {
+            ok = false;
+            break;
+          }
+          // raise M to the largest logit so far, row by row
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            float m = x[c];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) red[quarter * N + C * half + c] = m;
+          }
+          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+#pragma unroll
+          for (int c0 = 0; c0 < C; c0 += 8) {
+            float f[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int r = C * half + c0 + c;
+              const float m = fmaxf(fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])), M[c0 + c]);
+              f[c] = ex2(M[c0 + c] - m);
+              Z[c0 + c] *= f[c];
+              M[c0 + c] = m;
+            }
+            if (tile > un.t0) {
+#pragma unroll 1
+              for (int m = 0; m < 4; ++m) {
+                float o[8];
+                ptx::tmem_ld8(lane_base + kColO + N * m + c0, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o[c] *= f[c];
+                ptx::tmem_st8(lane_base + kColO + N * m + c0, o);
+              }
+            }
+          }
+          ptx::tmem_wait_st();
+          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);   // `red` is free again
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          x[c] = ex2(x[c] - M[c]);
+          Z[c] += x[c];
+        }
+        if (hurt) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if ((hurt >> c) & 1u) Z[c] = __int_as_float(0x7fc00000);
+        }
+#pragma unroll
+        for (int c = 0; c < C; c += 8)
+          *reinterpret_cast<uint4*>(pt + (c / 8) * 2048) = make_uint4(pack2(x[c], x[c + 1]), pack2(x[c + 2], x[c + 3]),
+                                                                    pack2(x[c + 4], x[c + 5]), pack2(x[c + 6], x[c + 7]));
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      // ---- the unit's sums
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float z = Z[c];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) red[quarter * N + C * half + c] = z;
+        if (lane == 0 && quarter == 0) row_mz[C * half + c].x = M[c];
+      }
+      const bool live = warp_wait(o_full, nu & 1, wt, 0xC32);
+      if (sid == 0) *broken = 0ull;
+      if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, !live)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      if (sid < N) row_mz[sid].y = (red[sid] + red[N + sid]) + (red[2 * N + sid] + red[3 * N + sid]);
+      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      const bool whole = un.parts == 1;
+      const int64_t row0 = (int64_t)un.b * t.T * t.H + (int64_t)un.rb * N;
+      if (whole ? p.lse && sid < rows : sid < rows && LCA_CHECK(t.err, u < p.slots, 0xD40)) {
+        const float2 mz = row_mz[sid];
+        if (whole) {
+          p.lse[row0 + sid] = mz.y == 0.f ? -INFINITY : kTreeLn2 * (mz.x + log2f(mz.y));
+        } else {
+          p.part_mz[2 * (u * N + sid)] = mz.x;
+          p.part_mz[2 * (u * N + sid) + 1] = mz.y;
+        }
+      }
+      for (int m = 0; m < 4; ++m) {
+        float o[C];
+        tmem_load<C>(lane_base + kColO + N * m, o);
+        ptx::tmem_wait_ld();
+        const int dim = 128 * m + tok;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int r = C * half + c;
+          if (r >= rows) break;
+          if (whole) {
+            const float z = row_mz[r].y;
+            p.out[(row0 + r) * kDC + dim] = __float2bfloat16_rn(z == 0.f ? 0.f : o[c] * (1.f / z));
+          } else if (LCA_CHECK(t.err, u < p.slots, 0xD41)) {
+            p.part_o[(u * N + r) * kDC + dim] = o[c];
+          }
+        }
+      }
+      ptx::tc_fence_before();
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace ttc
+}  // namespace lca

@@ -1,0 +1,81 @@
+"""How ragged batches of draft trees are cut into units (csrc/tree_schedule.cuh),
+on the CPU: the header's arithmetic, compiled for the host with one lane, over
+random batches.  Every (sequence, row block, tile) lies in exactly one unit, no
+partial lies past the workspace, and the units fill the CTAs within a stated
+bound."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+PROGRAM = r"""
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+#include <random>
+#include <vector>
+#include "tree_schedule.cuh"
+using namespace lca;
+struct One {
+  int lane() const { return 0; }
+  int count() const { return 1; }
+  int64_t sum(int64_t v) const { return v; }
+  int64_t scan(int64_t v) const { return v; }
+  int first(bool p) const { return p ? 0 : -1; }
+  int get(int v, int) const { return v; }
+  int64_t get(int64_t v, int) const { return v; }
+};
+int main() {
+  std::mt19937 rng(7);
+  auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+  for (int round = 0; round < 400; ++round) {
+    const int B = pick(1, round % 7 == 0 ? 700 : 40), G = round % 5 == 0 ? pick(1, 20) : 148;
+    const int N = round % 3 == 0 ? 16 : round % 3 == 1 ? 32 : 64, H = pick(1, 128), T = pick(1, 64);
+    const int span = 1 << pick(0, 17);
+    std::vector<TreeWork> ws(B);
+    int most = 1;
+    for (auto& w : ws) {
+      w = tree_work(pick(0, span), pick(0, T), H, N);
+      most = std::max(most, w.tiles);
+    }
+    auto seq = [&](int b) { return ws[b]; };
+    const One one;
+    int S = most;
+    int64_t best = INT64_MAX;
+    for (int k = 1; k <= kTreeMaxWaves; ++k) {
+      const int s = tree_least(one, seq, B, most, (int64_t)k * G);
+      if (s > 1 && s <= most && tree_units(one, seq, B, s - 1) <= (int64_t)k * G) return printf("not the least\n"), 1;
+      const int64_t c = tree_cost(k, s, most);
+      if (c < best) best = c, S = s;
+    }
+    std::vector<std::vector<int>> seen(B);
+    for (int b = 0; b < B; ++b) seen[b].assign((size_t)ws[b].rb * ws[b].tiles, 0);
+    const int64_t units = tree_units(one, seq, B, S);
+    for (int64_t u = 0; u < units; ++u) {
+      const TreeUnit x = tree_unit(one, seq, B, S, u);
+      if (x.b < 0 || x.t0 >= x.t1 || x.t1 - x.t0 > S || x.rb >= ws[x.b].rb || x.part >= x.parts)
+        return printf("unit %lld is none\n", (long long)u), 1;
+      if (x.parts > 1 && u >= (int64_t)kTreeMaxWaves * G) return printf("a slot past the workspace\n"), 1;
+      for (int t = x.t0; t < x.t1; ++t) ++seen[x.b][(size_t)x.rb * ws[x.b].tiles + t];
+    }
+    if (tree_unit(one, seq, B, S, units).b != -1) return printf("a unit too many\n"), 1;
+    for (auto& v : seen)
+      for (int c : v)
+        if (c != 1) return printf("a tile in %d units\n", c), 1;
+    if (best != INT64_MAX && units > (int64_t)kTreeMaxWaves * G) return printf("too many units\n"), 1;
+  }
+  printf("ok\n");
+  return 0;
+}
+"""
+
+
+def test_units_cover_every_tile_once(tmp_path):
+    src = tmp_path / "schedule.cpp"
+    src.write_text(PROGRAM)
+    exe = tmp_path / "schedule"
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I" + os.path.join(ROOT, "kv_compression_b200", "csrc"), "-o", str(exe),
+                    str(src)], check=True)
+    assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "ok\n"
