@@ -1,0 +1,399 @@
+// mass_tc_kernel.cuh -- accumulated attention weights with tcgen05 tensor cores
+// (bf16, d_c = 512, d_r = 64).
+//
+//   s[t] = decay prev[t] + sum_r 2^{(q[r] . [c_t | k_t]) log2 e - lse[r] log2 e}
+//
+// Work is a list of (sequence, 128-token tile, block of N query rows), row
+// blocks fastest, and each CTA takes one contiguous range of it.  A step is
+//   S^T[128 tokens x N rows] = [C | K]_tile . [q_c | q_r]^T     36 MMAs, M = 128, K = 16
+// into one of two TMEM buffers, then eight warps add each token's weights up
+// (a thread holds one token and half of the rows) while the next step's MMAs
+// run.  Nothing is written per (row, token): a token's sum leaves once.
+//
+// One operand stays in shared memory and the other streams through a ring of
+// [128][64] chunks:
+//   up to 128 rows   the queries stay (N = 16 .. 128) and the cache streams: it is read
+//                    once, at memory speed
+//   more rows        a tile of the cache stays and the query blocks (N = 128) stream, from
+//                    L2: the cache comes from memory once whatever the number of rows
+// A tile whose row blocks are split over CTAs gets one partial sum from each;
+// lca_mass_finish_kernel adds those in CTA order, so the result does not depend
+// on timing.
+//
+// Roles (320 threads): warp 0 loads, warp 1 issues the MMAs, warps 2-9 add.
+// Every wait is bounded, as in the tree kernel.
+#pragma once
+#include <cuda.h>
+
+#include "tree_simt_kernel.cuh"
+#include "tree_tc_kernel.cuh"
+
+namespace lca {
+namespace mtc {
+
+using ttc::kChunk;
+using ttc::Wait;
+constexpr int kThreads = ttc::kThreads;
+constexpr int kAddWarps = ttc::kSoftmaxWarps;
+constexpr int kBarAdd = 1;
+constexpr int kMaxSlots = 12;
+
+template <int N, bool kStream>       // kStream: the queries stream
+struct Layout {
+  static_assert(!kStream || N == 128, "streamed queries come 128 rows at a time");
+  static constexpr int kQChunk = N * 128;
+  static constexpr int kStay = kStream ? kChunk : kQChunk;                 // a chunk of the operand that stays
+  static constexpr int kSlots = N == 128 ? 4 : N == 64 ? 9 : N == 32 ? 11 : 12;
+  static constexpr int kOffRing = 9 * kStay;
+  static constexpr int kOffOff = kOffRing + kSlots * kChunk;               // float [2][N] offsets of the rows
+  static constexpr int kOffWord = kOffOff + 8 * N;                         // u64 [2][N] mask words
+  static constexpr int kOffPart = kOffWord + 16 * N;                       // float [128]
+  static constexpr int kOffBar = kOffPart + 512;
+  static constexpr int kBars = 2 * kMaxSlots + 7;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kBytes = kOffMisc + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kCols = N <= 16 ? 32 : N == 32 ? 64 : N == 64 ? 128 : 256;
+  static_assert(kAlloc <= 232448, "shared memory of one CTA");
+};
+
+struct Split {                  // one per sequence, for the finishing kernel
+  int64_t base;                 // first step
+  int tiles, rb;
+};
+
+struct Params {
+  CUtensorMap tm_c, tm_k;       // pools, box [64 rows][64]
+  CUtensorMap tm_qc, tm_qr;     // queries as [B T H rows][..], box [N rows][64]
+  MassParams m;
+  int G;
+  float* part;                  // [2 G][128]: a CTA's first and last tile, where it holds a share of it
+  Split* split;
+  uint64_t timeout_ns;
+  int debug_skip_load;
+};
+
+// Where a step lies, and the step after it.
+struct Step {
+  int b, tile, rb;
+  int tiles, rbs;               // of sequence b
+};
+
+template <int N, bool kStream>
+__global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_constant__ Params p) {
+  using L = Layout<N, kStream>;
+  constexpr int kSlots = L::kSlots;
+  constexpr int C = N / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t *full = bars, *empty = bars + kMaxSlots, *stay_full = bars + 2 * kMaxSlots, *stay_empty = stay_full + 1,
+           *s_full = stay_full + 2, *s_empty = stay_full + 4, *drain = stay_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  const TreeBatch& t = p.m.t;
+  const Wait wt = {abort_flag, t.err, p.timeout_ns};
+  const WarpLanes lanes;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(full + i, 1);
+      ptx::mbar_init(empty + i, 1);
+    }
+    ptx::mbar_init(stay_full, 1);
+    ptx::mbar_init(stay_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(s_full + i, 1);
+      ptx::mbar_init(s_empty + i, kAddWarps);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, L::kCols);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&p.tm_c);
+    ptx::prefetch_tmap(&p.tm_k);
+    ptx::prefetch_tmap(&p.tm_qc);
+    ptx::prefetch_tmap(&p.tm_qr);
+  }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  auto seq = [&](int b) {
+    const TreeLens l = tree_lens(t, b);
+    TreeWork w = tree_work(l.n, l.d, t.H, N);
+    if (l.d == 0 && l.n > 0) {        // nothing to add, but the old sums are scaled all the same
+      w.rb = 1;
+      w.tiles = (l.n + kTreeTile - 1) / kTreeTile;
+    }
+    return w;
+  };
+  const int64_t U = tree_units(lanes, seq, t.B, 1);
+  // CTA c of the G used (no more than there are steps): steps [c U / G, (c + 1) U / G)
+  const int64_t G = U < p.G ? U : p.G, c0 = blockIdx.x;
+  const int64_t u0 = c0 < G ? c0 * U / G : 0, u1 = c0 < G ? (c0 + 1) * U / G : 0;
+  Step st0 = {0, 0, 0, 1, 1};
+  if (u0 < u1) {
+    const TreeUnit x = tree_unit(lanes, seq, t.B, 1, u0);
+    const TreeWork w = seq(x.b);
+    st0 = Step{x.b, x.t0, x.rb, w.tiles, w.rb};
+  }
+  auto next = [&](Step& s) {
+    if (++s.rb < s.rbs) return;
+    s.rb = 0;
+    if (++s.tile < s.tiles) return;
+    s.tile = 0;
+    s.tiles = 0;
+    while (s.tiles == 0 && ++s.b < t.B) {
+      const TreeWork w = seq(s.b);
+      s.tiles = w.tiles;
+      s.rbs = w.rb;
+    }
+  };
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      int64_t nc = 0;
+      int ns = 0;
+      int64_t sent[kMaxSlots];
+#pragma unroll
+      for (int i = 0; i < kMaxSlots; ++i) sent[i] = 0;
+      bool ok = true;
+      Step s = st0;
+      int last_b = -1, last_tile = -1;
+      for (int64_t u = u0; u < u1 && ok; ++u, next(s)) {
+        const TreeLens l = tree_lens(t, s.b);
+        const int total = l.n + l.d, pos = s.tile * kTreeTile;
+        const int r0 = (int)tree_row(t, s.b, pos, 0xB06);
+        const int r1 = pos + 64 < total ? (int)tree_row(t, s.b, pos + 64, 0xB06) : r0;
+        const int qrow = (int)((int64_t)s.b * t.T * t.H + (int64_t)s.rb * N);
+        auto load_tile = [&](uint8_t* dst, int c, uint64_t* bar) {
+          const CUtensorMap* map = c < 8 ? &p.tm_c : &p.tm_k;
+          const int x = c < 8 ? 64 * c : 0;
+          ptx::tma_load_2d(dst, map, x, r0, bar);
+          ptx::tma_load_2d(dst + kChunk / 2, map, x, r1, bar);
+        };
+        auto load_q = [&](uint8_t* dst, int c, uint64_t* bar) {
+          ptx::tma_load_2d(dst, c < 8 ? &p.tm_qc : &p.tm_qr, c < 8 ? 64 * c : 0, qrow, bar);
+        };
+        if (s.b != last_b || (kStream && s.tile != last_tile)) {
+          last_b = s.b;
+          last_tile = s.tile;
+          if (ns > 0) ok = ttc::wait(stay_empty, (ns - 1) & 1, wt, 0xC40);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(stay_full, 9 * L::kStay);
+          for (int c = 0; c < 9; ++c) {
+            if constexpr (kStream) load_tile(smem + c * L::kStay, c, stay_full);
+            else load_q(smem + c * L::kStay, c, stay_full);
+          }
+          ++ns;
+        }
+        for (int c = 0; c < 9 && ok; ++c, ++nc) {
+          const int slot = (int)(nc % kSlots);
+          const int64_t use = nc / kSlots;
+          if (use > 0) ok = ttc::wait(empty + slot, (uint32_t)(use - 1) & 1, wt, 0xC41);
+          if (!ok) break;
+          if (p.debug_skip_load && nc == 0) continue;
+          ptx::mbar_arrive_expect_tx(full + slot, kChunk);
+          uint8_t* dst = smem + L::kOffRing + slot * kChunk;
+          if constexpr (kStream) load_q(dst, c, full + slot);
+          else load_tile(dst, c, full + slot);
+#pragma unroll
+          for (int q = 0; q < kMaxSlots; ++q)
+            if (q == slot) sent[q] = use + 1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (sent[i] > 0) ttc::wait(full + i, (uint32_t)(sent[i] - 1) & 1, wt, 0xC4F, false);
+      if (ns > 0) ttc::wait(stay_full, (ns - 1) & 1, wt, 0xC4F, false);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      constexpr uint32_t kId = ptx::idesc_bf16_f32(128, N, 0, 0);
+      const uint64_t d_stay = ptx::smem_desc(ptx::smem_u32(smem), 16, 1024, ptx::kSwizzle128B);
+      const uint64_t d_ring = ptx::smem_desc(ptx::smem_u32(smem + L::kOffRing), 16, 1024, ptx::kSwizzle128B);
+      int64_t nc = 0, i = 0;
+      int ns = 0;
+      bool ok = true;
+      Step s = st0;
+      int last_b = -1, last_tile = -1;
+      for (int64_t u = u0; u < u1 && ok; ++u, ++i) {
+        if (s.b != last_b || (kStream && s.tile != last_tile)) {
+          last_b = s.b;
+          last_tile = s.tile;
+          ok = ttc::wait(stay_full, ns & 1, wt, 0xC42);
+          ++ns;
+        }
+        const int buf = (int)(i & 1);
+        if (ok && i >= 2) ok = ttc::wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43);
+        for (int c = 0; c < 9 && ok; ++c, ++nc) {
+          const int slot = (int)(nc % kSlots);
+          ok = ttc::wait(full + slot, (uint32_t)(nc / kSlots) & 1, wt, 0xC44);
+          if (!ok) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t a = d_stay + (uint64_t)((c * L::kStay + 32 * k) >> 4);
+            const uint64_t r = d_ring + (uint64_t)((slot * kChunk + 32 * k) >> 4);
+            ptx::mma_bf16_ss(tmem + N * buf, kStream ? a : r, kStream ? r : a, kId, (c | k) != 0);
+          }
+          ptx::mma_commit(empty + slot);
+        }
+        if (!ok) break;
+        ptx::mma_commit(s_full + buf);
+        const int b = s.b, tile = s.tile;
+        next(s);
+        if (u + 1 < u1 && (s.b != b || (kStream && s.tile != tile))) ptx::mma_commit(stay_empty);
+      }
+      ptx::mma_commit(drain);
+      ttc::wait(drain, 0, wt, 0xC4E, false);
+    }
+  } else {
+    // ---------------------------------------------------------------- sums
+    const int sw = warp - 2, sid = tid - 64;
+    const int quarter = warp & 3, half = sw >> 2;
+    const int tok = 32 * quarter + lane;
+    const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + C * half;
+    float* off = reinterpret_cast<float*>(smem + L::kOffOff);
+    unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord);
+    float* part = reinterpret_cast<float*>(smem + L::kOffPart);
+    if (blockIdx.x == 0 && sw == 7) {
+      int64_t base = 0;
+      for (int b0 = 0; b0 < t.B; b0 += 32) {
+        const int b = b0 + lane;
+        TreeWork k = {0, 0};
+        if (b < t.B) {
+          k = seq(b);
+          if (tree_lens(t, b).bad) input_error(t.err, 0xB03);
+        }
+        const int64_t mine = (int64_t)k.rb * k.tiles, incl = base + lanes.scan(mine);
+        if (b < t.B) p.split[b] = Split{incl - mine, k.tiles, k.rb};
+        base = lanes.get(incl, 31);
+      }
+    }
+    Step s = st0;
+    int64_t i = 0;
+    int segment = 0;
+    bool from_start = s.rb == 0;
+    float acc = 0.f;
+    for (int64_t u = u0; u < u1; ++u, ++i) {
+      const TreeLens l = tree_lens(t, s.b);
+      const int buf = (int)(i & 1);
+      const int rows = min(N, l.d * t.H - s.rb * N);            // 0: nothing drafted
+      const int pos0 = s.tile * kTreeTile;
+      const bool special = pos0 + kTreeTile > l.n;
+      // this step's rows; one that adds nothing is marked by an infinite offset
+      bool none = false;
+      if (sid < N) {
+        float o = INFINITY;
+        if (sid < rows) {
+          const int r = s.rb * N + sid;
+          o = mass_offset(p.m.lse[(int64_t)s.b * t.T * t.H + r]);
+          if (special) words[buf * N + sid] = tree_word(t, s.b, r / t.H);
+        }
+        off[buf * N + sid] = o;
+        none = o == INFINITY;
+      }
+      bool live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45);
+      const bool gaps = ptx::named_bar_or(kBarAdd, 32 * kAddWarps, none || !live);
+      if (gaps && ptx::named_bar_or(kBarAdd, 32 * kAddWarps, !live)) break;
+      ptx::tc_fence_after();
+      const int node = pos0 + tok - l.n;
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int c0 = 0; c0 < C; c0 += (C < 32 ? C : 32)) {
+        constexpr int W = C < 32 ? C : 32;
+        float x[W];
+        ttc::tmem_load<W>(addr + N * buf + c0, x);
+        ptx::tmem_wait_ld();
+        const float* o = off + buf * N + C * half + c0;
+        if (!gaps && !special) {
+#pragma unroll
+          for (int c = 0; c < W; c += 2) {
+            const float2 o2 = *reinterpret_cast<const float2*>(o + c);
+            a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o2.x));
+            a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o2.y));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            const float oc = o[c];
+            bool sees = oc != INFINITY;
+            if (special && node >= 0)
+              sees = sees && node < l.d && ((words[buf * N + C * half + c0 + c] >> node) & 1ull);
+            if (sees) a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -oc));
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(s_empty + buf);
+      acc += a0 + a1;
+      const Step at = s;
+      next(s);
+      if (u + 1 == u1 || s.tile != at.tile || s.b != at.b) {
+        // the end of this CTA's share of a tile
+        if (half == 1) part[tok] = acc;
+        ptx::named_bar_sync(kBarAdd, 32 * kAddWarps);
+        if (half == 0) {
+          const float sum = acc + part[tok];
+          if (from_start && at.rb + 1 == at.rbs) {
+            if (pos0 + tok < l.n + l.d) mass_store(p.m, at.b, pos0 + tok, l.n, sum);
+          } else {
+            p.part[(2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0)) * kTreeTile + tok] = sum;
+          }
+        }
+        ptx::named_bar_sync(kBarAdd, 32 * kAddWarps);
+        acc = 0.f;
+        ++segment;
+        from_start = true;
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, L::kCols);
+}
+
+struct FinishParams {
+  MassParams m;
+  int G;
+  const float* part;
+  const Split* split;
+};
+
+// The tiles that more than one CTA had a share of: their shares added in CTA
+// order.  grid (blocks, B), a thread per token.
+__global__ void __launch_bounds__(kTreeTile) lca_mass_finish_kernel(const FinishParams p) {
+  ptx::griddep_wait();
+  const int b = blockIdx.y, tok = threadIdx.x;
+  const Split sp = p.split[b], last = p.split[p.m.t.B - 1];
+  const int64_t U = last.base + (int64_t)last.tiles * last.rb;
+  const int64_t G = U < p.G ? U : p.G;
+  const TreeLens l = tree_lens(p.m.t, b);
+  for (int tile = blockIdx.x; tile < sp.tiles; tile += gridDim.x) {
+    const int64_t u = sp.base + (int64_t)tile * sp.rb;
+    const int64_t lo = ((u + 1) * G - 1) / U, hi = ((u + sp.rb) * G - 1) / U;   // the CTAs of its first and last step
+    if (lo == hi) continue;
+    float sum = 0.f;
+    for (int64_t c = lo; c <= hi; ++c) sum += p.part[(2 * c + (c * U / G < u ? 1 : 0)) * kTreeTile + tok];
+    const int pos = tile * kTreeTile + tok;
+    if (pos < l.n + l.d) mass_store(p.m, b, pos, l.n, sum);
+  }
+}
+
+}  // namespace mtc
+}  // namespace lca

@@ -11,6 +11,7 @@
 
 #include "evict_kernel.cuh"
 #include "lca.h"
+#include "mass_tc_kernel.cuh"
 #include "plan.cuh"
 #include "tree_common.cuh"
 #include "tmap.cuh"
@@ -28,7 +29,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 constexpr size_t kMaxSmem = 232448;
 
 // ---------------------------------------------------------------- workspace
-// [TreeSplit x B][(M, Z) of every slot row][O of every slot row], each part
+// [a record for each sequence][(M, Z) of every slot row][O of every slot row], each part
 // 256-byte aligned.
 struct Workspace {
   int64_t slot_rows;      // rows of partials
@@ -56,6 +57,7 @@ Workspace workspace_of(const lca_plan* p, int T) {
   const int64_t parts = simt_parts(p, T);
   w.slot_rows = parts > 1 ? parts * p->B * round_up((int64_t)T * p->H, lca::kTreeSimtRows) : 0;
   if (tc_ok(p)) w.slot_rows = std::max<int64_t>(w.slot_rows, (int64_t)lca::kTreeMaxWaves * p->num_sms * tc_rows(p, T));
+  static_assert(sizeof(lca::mtc::Split) <= sizeof(lca::TreeSplit), "one record's room");
   w.mz = (size_t)round_up((int64_t)p->B * sizeof(lca::TreeSplit), 256);
   w.o = w.mz + (size_t)round_up(w.slot_rows * 2 * sizeof(float), 256);
   w.bytes = w.o + (size_t)w.slot_rows * p->d_c * sizeof(float);
@@ -214,6 +216,50 @@ lca_status run_mass_simt(const lca_plan* p, const lca::MassParams& mp, cudaStrea
   return launched();
 }
 
+// Up to 128 rows a sequence the queries stay in shared memory, in blocks of N;
+// with more they stream past each tile of the cache.
+template <int N, bool kStream>
+lca_status run_mass_tc(const lca_plan* p, const lca::MassParams& m, uint8_t* ws, const Workspace& w,
+                       cudaStream_t stream) {
+  namespace mtc = lca::mtc;
+  const TreeBatch& t = m.t;
+  mtc::Params mp;
+  std::memset(&mp, 0, sizeof(mp));
+  const uint64_t rows = (uint64_t)t.num_pages * (uint64_t)t.page_size, qrows = (uint64_t)t.B * t.T * t.H;
+  if (!lca::make_map(&mp.tm_c, t.c, lca::ttc::kDC, rows, 64) || !lca::make_map(&mp.tm_k, t.k, lca::ttc::kDR, rows, 64) ||
+      !lca::make_map(&mp.tm_qc, m.q_c, lca::ttc::kDC, qrows, N) || !lca::make_map(&mp.tm_qr, m.q_r, lca::ttc::kDR, qrows, N))
+    return LCA_ERR_CUDA;
+  mp.m = m;
+  mp.G = p->num_ctas > 0 ? p->num_ctas : p->num_sms;
+  mp.split = reinterpret_cast<mtc::Split*>(ws);
+  mp.part = reinterpret_cast<float*>(ws + w.o);
+  mp.timeout_ns = p->timeout_ns;
+  mp.debug_skip_load = p->debug_skip_load;
+  if (!allow_smem(mtc::lca_mass_tc_kernel<N, kStream>, mtc::Layout<N, kStream>::kAlloc)) return LCA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)mp.G, 1, 1);
+  cfg.blockDim = dim3(mtc::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = mtc::Layout<N, kStream>::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, mtc::lca_mass_tc_kernel<N, kStream>, mp) != cudaSuccess) return LCA_ERR_CUDA;
+  if (!kStream) return LCA_OK;                       // one row block: every tile is one CTA's
+  mtc::FinishParams fp = {};
+  fp.m = m;
+  fp.G = mp.G;
+  fp.part = mp.part;
+  fp.split = mp.split;
+  const int64_t tiles = ceil_div(t.cap, lca::kTreeTile);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, std::max<int64_t>(1, 4LL * p->num_sms / t.B)), (unsigned)t.B, 1);
+  cfg.blockDim = dim3(lca::kTreeTile, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, mtc::lca_mass_finish_kernel, fp) == cudaSuccess ? LCA_OK : LCA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -279,7 +325,17 @@ lca_status lca_attn_mass(lca_plan* p, const void* q_c, const void* q_r, int n_dr
   mp.stride = score_stride;
   mp.decay = decay;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p->kernel_pref > 1) return LCA_ERR_UNSUPPORTED;
+  const int pref = p->force_simt ? 1 : p->kernel_pref;
+  if (pref > 2 || (pref == 2 && !tc_ok(p))) return LCA_ERR_UNSUPPORTED;
+  if (tc_ok(p) && pref != 1) {
+    const int64_t r = (int64_t)n_draft * p->H;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (r <= 16) return run_mass_tc<16, false>(p, mp, ws, w, s);
+    if (r <= 32) return run_mass_tc<32, false>(p, mp, ws, w, s);
+    if (r <= 64) return run_mass_tc<64, false>(p, mp, ws, w, s);
+    if (r <= 128) return run_mass_tc<128, false>(p, mp, ws, w, s);
+    return run_mass_tc<128, true>(p, mp, ws, w, s);
+  }
   return p->dt == LCA_F32 ? run_mass_simt<float>(p, mp, s) : run_mass_simt<__nv_bfloat16>(p, mp, s);
 }
 

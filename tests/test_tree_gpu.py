@@ -116,7 +116,7 @@ def check_tree(x: Batch, out, lse, tc: bool):
         d = x.drafts[b]
         assert np.all(got[b, d:] == -77.0), "rows past the drafted tokens were written"
         err = np.abs(got[b, :d] - want[b, :d])
-        assert np.all(err <= eo[b, :d] + 1e-30), (b, float((err / (eo[b, :d] + 1e-30)).max()))
+        assert (err / (eo[b, :d] + 1e-30)).max(initial=0) <= 1, b
         if gz is not None:
             assert np.all(gz[b, d:] == -77.0)
             fine = np.isfinite(wz[b, :d])
@@ -131,7 +131,7 @@ def check_mass(x: Batch, scores, lse, prev, decay):
         m = len(s)
         assert np.all(got[b, m:] == -77.0), "positions past the sequence were written"
         err = np.abs(got[b, :m] - s)
-        assert np.all(err <= e + 1e-30), (b, float((err / (e + 1e-30)).max()))
+        assert (err / (e + 1e-30)).max(initial=0) <= 1, b
 
 
 # (H, T, lens, drafts, page, dtype, d_c, d_r)
@@ -256,7 +256,7 @@ def test_rows_that_see_nothing_and_masked_garbage(dtype, H, force):
             assert np.all(np.abs(got[:, i] - want[:, i]) <= eo[:, i] + 1e-30)
             fine = np.isfinite(wz[:, i])
             assert np.array_equal(gz[:, i][~fine], wz[:, i][~fine])
-            assert np.all(np.abs(gz[:, i] - wz[:, i])[fine] <= ez[:, i][fine])
+            assert np.all(np.abs(gz[:, i][fine] - wz[:, i][fine]) <= ez[:, i][fine])
         for b, (v, which) in bad.items():
             if which == "c":
                 assert np.isnan(got[b, [1, 3]][..., 3]).all() or np.isinf(v)
