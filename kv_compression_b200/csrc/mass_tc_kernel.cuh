@@ -43,11 +43,10 @@ struct Layout {
   static_assert(!kStream || N == 128, "streamed queries come 128 rows at a time");
   static constexpr int kQChunk = N * 128;
   static constexpr int kStay = kStream ? kChunk : kQChunk;                 // a chunk of the operand that stays
-  static constexpr int kSlots = N == 128 ? 4 : N == 64 ? 9 : N == 32 ? 11 : 12;
+  static constexpr int kSlots = N == 128 ? 5 : N == 64 ? 9 : N == 32 ? 11 : 12;
   static constexpr int kOffRing = 9 * kStay;
   static constexpr int kOffOff = kOffRing + kSlots * kChunk;               // float [2][N] offsets of the rows
-  static constexpr int kOffWord = kOffOff + 8 * N;                         // u64 [2][N] mask words
-  static constexpr int kOffPart = kOffWord + 16 * N;                       // float [128]
+  static constexpr int kOffPart = kOffOff + 8 * N;                         // float [128]
   static constexpr int kOffBar = kOffPart + 512;
   static constexpr int kBars = 2 * kMaxSlots + 7;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
@@ -223,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       constexpr uint32_t kId = ptx::idesc_bf16_f32(128, N, 0, 0);
       const uint64_t d_stay = ptx::smem_desc(ptx::smem_u32(smem), 16, 1024, ptx::kSwizzle128B);
       const uint64_t d_ring = ptx::smem_desc(ptx::smem_u32(smem + L::kOffRing), 16, 1024, ptx::kSwizzle128B);
-      int64_t nc = 0, i = 0;
-      int ns = 0;
-      bool ok = true;
+      int64_t i = 0;
+      int ns = 0, slot = 0, ph = 0;
+      bool ok = true, ready = false;
       Step s = st0;
       int last_b = -1, last_tile = -1;
       for (int64_t u = u0; u < u1 && ok; ++u, ++i) {
@@ -237,18 +236,27 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         }
         const int buf = (int)(i & 1);
         if (ok && i >= 2) ok = ttc::wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43);
-        for (int c = 0; c < 9 && ok; ++c, ++nc) {
-          const int slot = (int)(nc % kSlots);
-          ok = ttc::wait(full + slot, (uint32_t)(nc / kSlots) & 1, wt, 0xC44);
-          if (!ok) break;
-          ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t a = d_stay + (uint64_t)((c * L::kStay + 32 * k) >> 4);
-            const uint64_t r = d_ring + (uint64_t)((slot * kChunk + 32 * k) >> 4);
-            ptx::mma_bf16_ss(tmem + N * buf, kStream ? a : r, kStream ? r : a, kId, (c | k) != 0);
+        for (int c = 0; c < 9; ++c) {
+          // the next chunk's barrier is probed before this one's MMAs (see the tree kernel)
+          if (!ready) ok = ok && ttc::wait(full + slot, ph, wt, 0xC44);
+          ptx::tc_fence_after();
+          int ahead = slot + 1, aph = ph;
+          if (ahead == kSlots) {
+            ahead = 0;
+            aph ^= 1;
           }
+          ready = ptx::mbar_test_wait(full + ahead, aph);
+          if (!ok) break;
+          const uint64_t a = d_stay + (uint64_t)((c * L::kStay) >> 4);
+          const uint64_t r = d_ring + (uint64_t)((slot * kChunk) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_bf16_ss(tmem + N * buf, (kStream ? a : r) + (uint64_t)((32 * k) >> 4),
+                             (kStream ? r : a) + (uint64_t)((32 * k) >> 4), kId, (c | k) != 0);
           ptx::mma_commit(empty + slot);
+          slot = ahead;
+          ph = aph;
         }
         if (!ok) break;
         ptx::mma_commit(s_full + buf);
@@ -266,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     const int tok = 32 * quarter + lane;
     const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + C * half;
     float* off = reinterpret_cast<float*>(smem + L::kOffOff);
-    unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord);
     float* part = reinterpret_cast<float*>(smem + L::kOffPart);
     if (blockIdx.x == 0 && sw == 7) {
       int64_t base = 0;
@@ -285,32 +292,42 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     Step s = st0;
     int64_t i = 0;
     int segment = 0;
-    bool from_start = s.rb == 0;
+    bool from_start = s.rb == 0, fresh = true;
     float acc = 0.f;
+    TreeLens l = tree_lens(t, s.b);
+    // a row's offset; rows that add nothing have an infinite one.  Read a step ahead.
+    auto offset = [&](const Step& at, int d) {
+      const int r = at.rb * N + sid;
+      return sid < N && r < d * t.H ? mass_offset(p.m.lse[(int64_t)at.b * t.T * t.H + r]) : INFINITY;
+    };
+    float o_next = u0 < u1 ? offset(s, l.d) : INFINITY;
+    unsigned long long vis = ~0ull;                    // the nodes that see this thread's token
     for (int64_t u = u0; u < u1; ++u, ++i) {
-      const TreeLens l = tree_lens(t, s.b);
       const int buf = (int)(i & 1);
-      const int rows = min(N, l.d * t.H - s.rb * N);            // 0: nothing drafted
       const int pos0 = s.tile * kTreeTile;
-      const bool special = pos0 + kTreeTile > l.n;
-      // this step's rows; one that adds nothing is marked by an infinite offset
-      bool none = false;
-      if (sid < N) {
-        float o = INFINITY;
-        if (sid < rows) {
-          const int r = s.rb * N + sid;
-          o = mass_offset(p.m.lse[(int64_t)s.b * t.T * t.H + r]);
-          if (special) words[buf * N + sid] = tree_word(t, s.b, r / t.H);
-        }
-        off[buf * N + sid] = o;
-        none = o == INFINITY;
+      const bool special = pos0 + kTreeTile > l.n;     // drafted tokens, or the end, in this tile
+      if (sid < N) off[buf * N + sid] = o_next;
+      const bool none = sid < N && o_next == INFINITY;
+      const Step at = s;
+      const TreeLens lat = l;
+      next(s);
+      if (u + 1 < u1) {
+        if (s.b != at.b) l = tree_lens(t, s.b);
+        o_next = offset(s, l.d);
       }
-      bool live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45);
+      if (fresh && special) {
+        const int node = pos0 + tok - lat.n;
+        vis = node < 0 ? ~0ull : 0ull;
+        if (node >= 0 && node < lat.d)
+          for (int j = 0; j < lat.d; ++j) vis |= ((tree_word(t, at.b, j) >> node) & 1ull) << j;
+      }
+      fresh = false;
+      const bool live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45);
       const bool gaps = ptx::named_bar_or(kBarAdd, 32 * kAddWarps, none || !live);
       if (gaps && ptx::named_bar_or(kBarAdd, 32 * kAddWarps, !live)) break;
       ptx::tc_fence_after();
-      const int node = pos0 + tok - l.n;
       float a0 = 0.f, a1 = 0.f;
+      int node_of = (at.rb * N + C * half) / t.H, in_node = (at.rb * N + C * half) - node_of * t.H;
 #pragma unroll
       for (int c0 = 0; c0 < C; c0 += (C < 32 ? C : 32)) {
         constexpr int W = C < 32 ? C : 32;
@@ -320,19 +337,22 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         const float* o = off + buf * N + C * half + c0;
         if (!gaps && !special) {
 #pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            const float2 o2 = *reinterpret_cast<const float2*>(o + c);
-            a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o2.x));
-            a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o2.y));
+          for (int c = 0; c < W; c += 4) {
+            const float4 o4 = *reinterpret_cast<const float4*>(o + c);
+            a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o4.x));
+            a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o4.y));
+            a0 += ttc::ex2(fmaf(x[c + 2], kTreeLog2e, -o4.z));
+            a1 += ttc::ex2(fmaf(x[c + 3], kTreeLog2e, -o4.w));
           }
         } else {
 #pragma unroll
           for (int c = 0; c < W; ++c) {
             const float oc = o[c];
-            bool sees = oc != INFINITY;
-            if (special && node >= 0)
-              sees = sees && node < l.d && ((words[buf * N + C * half + c0 + c] >> node) & 1ull);
-            if (sees) a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -oc));
+            if (oc != INFINITY && ((vis >> node_of) & 1ull)) a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -oc));
+            if (++in_node == t.H) {
+              in_node = 0;
+              ++node_of;
+            }
           }
         }
       }
@@ -340,8 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(s_empty + buf);
       acc += a0 + a1;
-      const Step at = s;
-      next(s);
       if (u + 1 == u1 || s.tile != at.tile || s.b != at.b) {
         // the end of this CTA's share of a tile
         if (half == 1) part[tok] = acc;
@@ -349,15 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         if (half == 0) {
           const float sum = acc + part[tok];
           if (from_start && at.rb + 1 == at.rbs) {
-            if (pos0 + tok < l.n + l.d) mass_store(p.m, at.b, pos0 + tok, l.n, sum);
+            if (pos0 + tok < lat.n + lat.d) mass_store(p.m, at.b, pos0 + tok, lat.n, sum);
           } else {
             p.part[(2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0)) * kTreeTile + tok] = sum;
           }
         }
-        ptx::named_bar_sync(kBarAdd, 32 * kAddWarps);
         acc = 0.f;
+        vis = ~0ull;
         ++segment;
-        from_start = true;
+        from_start = fresh = true;
       }
     }
   }

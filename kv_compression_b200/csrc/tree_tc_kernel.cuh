@@ -300,44 +300,61 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(smem + L::kOffQ), 16, 1024, ptx::kSwizzle128B);
     const uint64_t d_ct = ptx::smem_desc(ptx::smem_u32(smem), kChunk, 1024, ptx::kSwizzle128B);
     const uint64_t d_p = ptx::smem_desc(ptx::smem_u32(smem + L::kOffP), 128, 2048, ptx::kSwizzleNone);
-    int64_t np = 0;
-    int it = 0, nq = 0;
+    // A probe of a barrier costs the issuing thread about 160 cycles before it
+    // may issue again, more than the MMAs in flight cover; so the next load's
+    // barrier is probed before the MMAs of the load at hand are issued, and
+    // looked at after them.
+    int it = 0, nq = 0, s0 = 0, ph = 0;     // tiles; slot of the tile's first load and the parity of its phase
     bool ok = true;
+    auto load_bar = [&](int i, int& parity) -> uint64_t* {   // load i of the tile at hand: K, or a column slot
+      if (i == kKAt) {
+        parity = it & 1;
+        return k_full;
+      }
+      int slot = s0 + (i < kKAt ? i : i - 1);
+      parity = ph;
+      if (slot >= kSlots) {
+        slot -= kSlots;
+        parity ^= 1;
+      }
+      return full + slot;
+    };
+    bool ready = false;
     for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
       if (lane == 0) {
         ok = wait(q_full, nq & 1, wt, 0xC20);
         ++nq;
-        for (int tile = un.t0; tile < un.t1 && ok; ++tile, ++it) {
-          bool acc = false;
-          for (int i = 0; i < 5 && ok; ++i) {
-            if (i == kKAt) {
-              ok = wait(k_full, it & 1, wt, 0xC21);
-              if (!ok) break;
-              ptx::tc_fence_after();
+        for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+          for (int i = 0; i < 5; ++i) {
+            int parity;
+            uint64_t* bar = load_bar(i, parity);
+            if (!ready) ok = ok && wait(bar, parity, wt, 0xC22);
+            ptx::tc_fence_after();
+            ready = false;
+            if (i < 4) {
+              uint64_t* ahead = load_bar(i + 1, parity);
+              ready = ptx::mbar_test_wait(ahead, parity);
+            }
+            if (!ok) continue;
+            if (i == kKAt) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
                 ptx::mma_bf16_ss(tmem + kColS, d_k + (uint64_t)((32 * k) >> 4),
-                                 d_q + (uint64_t)((8 * L::kQChunk + 32 * k) >> 4), kIdS, acc);
-                acc = true;
-              }
+                                 d_q + (uint64_t)((8 * L::kQChunk + 32 * k) >> 4), kIdS, (i | k) != 0);
               if (!L::kAlias) ptx::mma_commit(k_empty);
               continue;
             }
             const int m = i < kKAt ? i : i - 1;
-            const int slot = (int)((np + m) % kSlots);
-            ok = wait(full + slot, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC22);
-            if (!ok) break;
-            ptx::tc_fence_after();
+            const uint64_t a = d_c + (uint64_t)(((bar - full) * kSlot) >> 4);
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                ptx::mma_bf16_ss(tmem + kColS, d_c + (uint64_t)((slot * kSlot + ch * kChunk + 32 * k) >> 4),
-                                 d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, acc);
-                acc = true;
-              }
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_bf16_ss(tmem + kColS, a + (uint64_t)((ch * kChunk + 32 * k) >> 4),
+                                 d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, (i | ch | k) != 0);
           }
           if (!ok) break;
           ptx::mma_commit(s_full);
@@ -346,17 +363,31 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t first = tile > un.t0 ? 1u : 0u;
+          const int here = s0;
+          s0 += 4;                          // the next tile's first load
+          if (s0 >= kSlots) {
+            s0 -= kSlots;
+            ph ^= 1;
+          }
+          ++it;
+#pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const int slot = (int)((np + m) % kSlots);
+            int slot = here + m;
+            if (slot >= kSlots) slot -= kSlots;
+            if (m == 3) {
+              int parity;
+              uint64_t* ahead = load_bar(0, parity);
+              ready = ptx::mbar_test_wait(ahead, parity);
+            }
+            const uint64_t a = d_ct + (uint64_t)((slot * kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              ptx::mma_bf16_ss(tmem + kColO + N * m, d_ct + (uint64_t)((slot * kSlot + 2048 * k) >> 4),
-                               d_p + (uint64_t)((256 * k) >> 4), kIdO, k > 0 ? 1u : first);
+              ptx::mma_bf16_ss(tmem + kColO + N * m, a + (uint64_t)((2048 * k) >> 4), d_p + (uint64_t)((256 * k) >> 4),
+                               kIdO, k > 0 ? 1u : first);
             ptx::mma_commit(empty + slot);
           }
           if (L::kAlias) ptx::mma_commit(k_empty);
           if (tile + 1 == un.t1) ptx::mma_commit(o_full);
-          np += 4;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
