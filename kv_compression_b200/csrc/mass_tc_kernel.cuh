@@ -218,36 +218,40 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t kId = ptx::idesc_bf16_f32(128, N, 0, 0);
-      const uint64_t d_stay = ptx::smem_desc(ptx::smem_u32(smem), 16, 1024, ptx::kSwizzle128B);
-      const uint64_t d_ring = ptx::smem_desc(ptx::smem_u32(smem + L::kOffRing), 16, 1024, ptx::kSwizzle128B);
-      int64_t i = 0;
-      int ns = 0, slot = 0, ph = 0;
-      bool ok = true, ready = false;
-      Step s = st0;
-      int last_b = -1, last_tile = -1;
-      for (int64_t u = u0; u < u1 && ok; ++u, ++i) {
-        if (s.b != last_b || (kStream && s.tile != last_tile)) {
-          last_b = s.b;
-          last_tile = s.tile;
-          ok = ttc::wait(stay_full, ns & 1, wt, 0xC42);
-          ++ns;
-        }
-        const int buf = (int)(i & 1);
-        if (ok && i >= 2) ok = ttc::wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43);
+    // The whole warp runs this and one elected lane issues; the next chunk's barrier is probed
+    // before the MMAs of the chunk at hand (as in the tree kernel).
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, N, 0, 0);
+    const uint64_t d_stay = ptx::smem_desc(ptx::smem_u32(smem), 16, 1024, ptx::kSwizzle128B);
+    const uint64_t d_ring = ptx::smem_desc(ptx::smem_u32(smem + L::kOffRing), 16, 1024, ptx::kSwizzle128B);
+    int64_t i = 0;
+    int ns = 0, slot = 0, ph = 0;
+    bool ok = true, ready = false;
+    Step s = st0;
+    int last_b = -1, last_tile = -1;
+    for (int64_t u = u0; u < u1 && ok; ++u, ++i) {
+      if (s.b != last_b || (kStream && s.tile != last_tile)) {
+        last_b = s.b;
+        last_tile = s.tile;
+        ok = ttc::warp_wait(stay_full, ns & 1, wt, 0xC42);
+        ++ns;
+      }
+      const int b = s.b, tile = s.tile;
+      next(s);
+      const bool leaves = u + 1 < u1 && (s.b != b || (kStream && s.tile != tile));   // the operand that stays does not
+      const int buf = (int)(i & 1);
+      if (i >= 2) ok = ttc::warp_wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43) && ok;
 #pragma unroll
-        for (int c = 0; c < 9; ++c) {
-          // the next chunk's barrier is probed before this one's MMAs (see the tree kernel)
-          if (!ready) ok = ok && ttc::wait(full + slot, ph, wt, 0xC44);
-          ptx::tc_fence_after();
-          int ahead = slot + 1, aph = ph;
-          if (ahead == kSlots) {
-            ahead = 0;
-            aph ^= 1;
-          }
-          ready = ptx::mbar_test_wait(full + ahead, aph);
-          if (!ok) break;
+      for (int c = 0; c < 9; ++c) {
+        if (!__all_sync(0xffffffffu, ready)) ok = ttc::warp_wait(full + slot, ph, wt, 0xC44) && ok;
+        ptx::tc_fence_after();
+        int ahead = slot + 1, aph = ph;
+        if (ahead == kSlots) {
+          ahead = 0;
+          aph ^= 1;
+        }
+        ready = ptx::mbar_test_wait(full + ahead, aph);
+        if (!ok) break;
+        if (ptx::elect_one()) {
           const uint64_t a = d_stay + (uint64_t)((c * L::kStay) >> 4);
           const uint64_t r = d_ring + (uint64_t)((slot * kChunk) >> 4);
 #pragma unroll
@@ -255,18 +259,18 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
             ptx::mma_bf16_ss(tmem + N * buf, (kStream ? a : r) + (uint64_t)((32 * k) >> 4),
                              (kStream ? r : a) + (uint64_t)((32 * k) >> 4), kId, (c | k) != 0);
           ptx::mma_commit(empty + slot);
-          slot = ahead;
-          ph = aph;
+          if (c == 8) {
+            ptx::mma_commit(s_full + buf);
+            if (leaves) ptx::mma_commit(stay_empty);
+          }
         }
-        if (!ok) break;
-        ptx::mma_commit(s_full + buf);
-        const int b = s.b, tile = s.tile;
-        next(s);
-        if (u + 1 < u1 && (s.b != b || (kStream && s.tile != tile))) ptx::mma_commit(stay_empty);
+        __syncwarp();
+        slot = ahead;
+        ph = aph;
       }
-      ptx::mma_commit(drain);
-      ttc::wait(drain, 0, wt, 0xC4E, false);
     }
+    if (ptx::elect_one()) ptx::mma_commit(drain);
+    ttc::wait(drain, 0, wt, 0xC4E, false);
   } else {
     // ---------------------------------------------------------------- sums
     const int sw = warp - 2, sid = tid - 64;

@@ -24,8 +24,13 @@
 // K's place, which is read by then.  N <= 32 has a fifth slot and P its own.
 //
 // The reference M of a row rises only when a logit exceeds it by more than 2^8
-// (then Z and O^T are scaled): one barrier with an OR over the softmax warps
-// per tile decides that.
+// (then Z and O^T are scaled).  Whether one does is not agreed on beforehand: a
+// barrier of the softmax warps cost about 500 cycles a tile.  A thread that
+// meets such a logit says so beside its arrival; the MMA issuer, which waits for
+// all arrivals anyway, then hands the tile back instead of going on to O, and
+// the softmax warps raise M and form P again.  (A unit's first tile always
+// raises M and does so at once.)  A tile's weights join Z when the next event
+// shows that it was not handed back.
 //
 // Tokens a row does not see get weight 0; because 0 x NaN is not 0, rows of
 // the tile that hold no token are zeroed in shared memory, and a drafted row
@@ -53,10 +58,10 @@ constexpr int kSlot = 2 * kChunk;           // 128 latent dims of a tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (2 + kSoftmaxWarps);
 constexpr int kMaxSlots = 5;
-constexpr int kBarSoftmax = 1;              // named barrier of the softmax warps
 constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
 constexpr float kRaise = 8.f;
 constexpr int kErrTimeout = 1;
+constexpr int kProbes = 64;
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
 template <int N>
@@ -72,8 +77,8 @@ struct Layout {
   static constexpr int kOffM = kOffRed + 16 * N;       // float2 [N]: the rows' (M, Z)
   static constexpr int kOffBar = kOffM + 8 * N;
   static constexpr int kBars = 2 * kMaxSlots + 8;
-  static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S; nodes with a broken row
-  static constexpr int kBytes = kOffMisc + 32;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S of k waves; nodes with a broken row;
+  static constexpr int kBytes = kOffMisc + 48;         // the event whose tile has to come back, the event it did
   static constexpr int kAlloc = kBytes + 1024;         // slack for the 1 KB alignment
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
@@ -111,14 +116,16 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, const Wai
     }
   }
 }
-// A bounded wait of one thread; `warp_wait` the same for a whole warp, which leaves it together.
+// A bounded wait of one thread; `warp_wait` the same for a whole warp, which leaves it together.  Plain probes
+// first: one with a suspend-time hint may wake late, and these hand-offs set the pace.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Wait& w, int where, bool honour = true) {
-  return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity, w, where, honour);
+#pragma unroll 1
+  for (int i = 0; i < kProbes; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, w, where, honour);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Wait& w, int where) {
-  bool ok = ptx::mbar_try_wait(bar, parity);
-  if (!ok) ok = wait_slow(bar, parity, w, where, true);
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, wait(bar, parity, w, where));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -155,12 +162,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t *full = bars, *empty = bars + kMaxSlots, *k_full = bars + 2 * kMaxSlots, *k_empty = k_full + 1,
-           *q_full = k_full + 2, *q_empty = k_full + 3, *s_full = k_full + 4, *p_full = k_full + 5,
-           *o_full = k_full + 6, *drain = k_full + 7;
+           *q_full = k_full + 2, *q_empty = k_full + 3, *drain = k_full + 4,
+           *event = k_full + 5,       // for the softmax: S of a tile is there, a tile comes back, O is complete
+           *p_full = k_full + 6, *meet = k_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   int* s_least = reinterpret_cast<int*>(smem + L::kOffMisc + 8);       // [kTreeMaxWaves]
   unsigned long long* broken = reinterpret_cast<unsigned long long*>(smem + L::kOffMisc + 24);
+  volatile int* too_high = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 32);
+  volatile int* come_back = too_high + 1;
   const TreeBatch& t = p.t;
   const Wait wt = {abort_flag, t.err, p.timeout_ns};
   const WarpLanes lanes;
@@ -174,12 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     ptx::mbar_init(k_empty, 1);
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
-    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(event, 1);
     ptx::mbar_init(p_full, kSoftmaxWarps);
-    ptx::mbar_init(o_full, 1);
+    ptx::mbar_init(meet, kSoftmaxWarps);
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     *broken = 0ull;
+    *too_high = *come_back = -1;
     ptx::fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -300,18 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(smem + L::kOffQ), 16, 1024, ptx::kSwizzle128B);
     const uint64_t d_ct = ptx::smem_desc(ptx::smem_u32(smem), kChunk, 1024, ptx::kSwizzle128B);
     const uint64_t d_p = ptx::smem_desc(ptx::smem_u32(smem + L::kOffP), 128, 2048, ptx::kSwizzleNone);
-    // A probe of a barrier costs the issuing thread about 160 cycles before it
-    // may issue again, more than the MMAs in flight cover; so the next load's
-    // barrier is probed before the MMAs of the load at hand are issued, and
-    // looked at after them.
-    int it = 0, nq = 0, s0 = 0, ph = 0;     // tiles; slot of the tile's first load and the parity of its phase
-    bool ok = true;
+    // The whole warp runs this, and one elected lane issues: the operands' descriptors then
+    // stay in uniform registers (an MMA every 53 cycles; 77 from a branch that one lane takes).
+    // The next load's barrier is probed before the MMAs of the load at hand and looked at
+    // after them: a probe takes longer than the MMAs in flight cover.
+    int it = 0, nq = 0, s0 = 0, ph = 0, ev = 0, np = 0;   // tiles, query blocks; slot of the tile's first load and the
+    bool ok = true, ready = false;                         // parity of its phase; events, arrivals of P
     auto load_bar = [&](int i, int& parity) -> uint64_t* {   // load i of the tile at hand: K, or a column slot
       if (i == kKAt) {
         parity = it & 1;
         return k_full;
       }
-      int slot = s0 + (i < kKAt ? i : i - 1);
+      int slot = (kSlots == 4 ? 0 : s0) + (i < kKAt ? i : i - 1);
       parity = ph;
       if (slot >= kSlots) {
         slot -= kSlots;
@@ -319,83 +330,98 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
       }
       return full + slot;
     };
-    bool ready = false;
     for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
-      if (lane == 0) {
-        ok = wait(q_full, nq & 1, wt, 0xC20);
-        ++nq;
-        for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
+      ok = warp_wait(q_full, nq & 1, wt, 0xC20);
+      ++nq;
+      for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
 #pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            int parity;
-            uint64_t* bar = load_bar(i, parity);
-            if (!ready) ok = ok && wait(bar, parity, wt, 0xC22);
-            ptx::tc_fence_after();
-            ready = false;
-            if (i < 4) {
-              uint64_t* ahead = load_bar(i + 1, parity);
-              ready = ptx::mbar_test_wait(ahead, parity);
-            }
-            if (!ok) continue;
+        for (int i = 0; i < 5; ++i) {
+          int parity;
+          uint64_t* bar = load_bar(i, parity);
+          if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(bar, parity, wt, 0xC22) && ok;
+          ptx::tc_fence_after();
+          ready = false;
+          if (i < 4) {
+            uint64_t* ahead = load_bar(i + 1, parity);
+            ready = ptx::mbar_test_wait(ahead, parity);
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) {
             if (i == kKAt) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 ptx::mma_bf16_ss(tmem + kColS, d_k + (uint64_t)((32 * k) >> 4),
                                  d_q + (uint64_t)((8 * L::kQChunk + 32 * k) >> 4), kIdS, (i | k) != 0);
               if (!L::kAlias) ptx::mma_commit(k_empty);
-              continue;
+            } else {
+              const int m = i < kKAt ? i : i - 1;
+              const uint64_t a = d_c + (uint64_t)(((bar - full) * kSlot) >> 4);
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  ptx::mma_bf16_ss(tmem + kColS, a + (uint64_t)((ch * kChunk + 32 * k) >> 4),
+                                   d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, (i | ch | k) != 0);
             }
-            const int m = i < kKAt ? i : i - 1;
-            const uint64_t a = d_c + (uint64_t)(((bar - full) * kSlot) >> 4);
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_bf16_ss(tmem + kColS, a + (uint64_t)((ch * kChunk + 32 * k) >> 4),
-                                 d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, (i | ch | k) != 0);
-          }
-          if (!ok) break;
-          ptx::mma_commit(s_full);
-          if (tile + 1 == un.t1) ptx::mma_commit(q_empty);
-          ok = wait(p_full, it & 1, wt, 0xC23);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint32_t first = tile > un.t0 ? 1u : 0u;
-          const int here = s0;
-          s0 += 4;                          // the next tile's first load
-          if (s0 >= kSlots) {
-            s0 -= kSlots;
-            ph ^= 1;
-          }
-          ++it;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            int slot = here + m;
-            if (slot >= kSlots) slot -= kSlots;
-            if (m == 3) {
-              int parity;
-              uint64_t* ahead = load_bar(0, parity);
-              ready = ptx::mbar_test_wait(ahead, parity);
+            if (i == 4) {
+              ptx::mma_commit(event);
+              if (tile + 1 == un.t1) ptx::mma_commit(q_empty);
             }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ok = warp_wait(p_full, np++ & 1, wt, 0xC23);
+        if (ok && __shfl_sync(0xffffffffu, *too_high, 0) == ev) {
+          ++ev;
+          if (lane == 0) {
+            *come_back = ev;
+            ptx::mbar_arrive(event);
+          }
+          __syncwarp();
+          ok = warp_wait(p_full, np++ & 1, wt, 0xC24);
+        }
+        ++ev;
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t first = tile > un.t0 ? 1u : 0u;
+        const int here = kSlots == 4 ? 0 : s0;
+        s0 += 4;                            // the next tile's first load
+        if (s0 >= kSlots) {
+          s0 -= kSlots;
+          ph ^= 1;
+        }
+        ++it;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          int slot = here + m;
+          if (slot >= kSlots) slot -= kSlots;
+          if (m == 3) {
+            int parity;
+            uint64_t* ahead = load_bar(0, parity);
+            ready = ptx::mbar_test_wait(ahead, parity);
+          }
+          if (ptx::elect_one()) {
             const uint64_t a = d_ct + (uint64_t)((slot * kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               ptx::mma_bf16_ss(tmem + kColO + N * m, a + (uint64_t)((2048 * k) >> 4), d_p + (uint64_t)((256 * k) >> 4),
                                kIdO, k > 0 ? 1u : first);
             ptx::mma_commit(empty + slot);
+            if (m == 3) {
+              if (L::kAlias) ptx::mma_commit(k_empty);
+              if (tile + 1 == un.t1) ptx::mma_commit(event);
+            }
           }
-          if (L::kAlias) ptx::mma_commit(k_empty);
-          if (tile + 1 == un.t1) ptx::mma_commit(o_full);
+          __syncwarp();
         }
+        if (tile + 1 == un.t1) ++ev;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (lane == 0) {            // and every MMA
-      ptx::mma_commit(drain);
-      wait(drain, 0, wt, 0xC2F, false);
-    }
+    if (ptx::elect_one()) ptx::mma_commit(drain);   // and every MMA
+    wait(drain, 0, wt, 0xC2F, false);
   } else {
     // ---------------------------------------------------------------- softmax
     const int sw = warp - 2;
@@ -408,8 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     float2* row_mz = reinterpret_cast<float2*>(smem + L::kOffM);
     uint8_t* pt = smem + L::kOffP + (C / 8) * half * 2048 + tok * 16;
     int64_t np = 0;
-    int it = 0, nu = 0;
+    int ev = 0, met = 0;        // events seen; meetings of the softmax warps
     bool ok = true;
+    // A barrier of the softmax warps whose wait is bounded: a warp that leaves on an error leaves none behind.
+    auto meeting = [&] {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(meet);
+      ok = warp_wait(meet, met++ & 1, wt, 0xC33) && ok;
+      return ok;
+    };
     // the sequences' records for the merge, by the first CTA
     if (blockIdx.x == 0 && sw == 7) {
       int64_t base = 0;
@@ -428,34 +461,45 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
         base = lanes.get(incl, 31);
       }
     }
-    for (int64_t u = blockIdx.x; ok; u += p.G, ++nu) {
+    for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
       const TreeLens l = tree_lens(t, un.b);
       const int total = l.n + l.d;
       const int rows = min(N, l.d * t.H - un.rb * N);
-      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);    // the last unit's words and sums are read
+      if (!meeting()) break;                           // the last unit's words and sums are read
       if (sid < N) words[sid] = sid < rows ? tree_word(t, un.b, (un.rb * N + sid) / t.H) : 0ull;
-      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
-      float M[C], Z[C];
+      if (!meeting()) break;
+      float nM[C], Z[C], x[C];    // -M in units of log2; x: the weights not yet in Z
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        M[c] = kEmpty;
-        Z[c] = 0.f;
+        nM[c] = -kEmpty;
+        Z[c] = x[c] = 0.f;
       }
-      for (int tile = un.t0; tile < un.t1; ++tile, ++it, np += 4) {
-        const int pos0 = tile * kTreeTile;
-        bool live = warp_wait(s_full, it & 1, wt, 0xC30);
+      // one event after another: S of the next tile, the tile at hand once more, or the end
+      bool special = false;
+      for (int tile = un.t0 - 1;;) {
+        const bool live = warp_wait(event, ev & 1, wt, 0xC30);
         ptx::tc_fence_after();
-        float x[C];
+        const bool again = *come_back == ev;
+        if (!again) {
+#pragma unroll
+          for (int c = 0; c < C; c += 2)
+            ptx::f32x2_split(ptx::add_f32x2(ptx::f32x2(Z[c], Z[c + 1]), ptx::f32x2(x[c], x[c + 1])), Z[c], Z[c + 1]);
+          if (tile >= un.t0) np += 4;
+          ++tile;
+        }
+        ok = live;
+        if (!ok || tile == un.t1) break;
+        const int pos0 = tile * kTreeTile;
         tmem_load<C>(lane_base + kColS, x);
-        ptx::tmem_wait_ld();
-        const bool special = pos0 + kTreeTile > l.n;           // drafted tokens, or the end, in this tile
+        special = pos0 + kTreeTile > l.n;                      // drafted tokens, or the end, in this tile
+        const bool raise = again || tile == un.t0;
         uint32_t hurt = 0;                                     // rows that see this thread's broken token
         if (special) {
           // zero what is no token, and drafted rows that hold an infinity or NaN
           for (int m = 0; m < 4; ++m)
-            live = warp_wait(full + (np + m) % kSlots, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC31) && live;
+            ok = warp_wait(full + (np + m) % kSlots, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC31) && ok;
           for (int r = sw; r < kTreeTile; r += kSoftmaxWarps) {
             const int pos = pos0 + r;
             if (pos < l.n) continue;
@@ -474,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             }
             if (bad && pos < total && lane == 0) atomicOr(broken, 1ull << (pos - l.n));
           }
-          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+          if (!meeting()) break;
+        }
+        ptx::tmem_wait_ld();
+        if (special) {
           const int node = pos0 + tok - l.n;
           if (node >= 0) {
             const bool in = node < l.d;
@@ -487,36 +534,26 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             }
           }
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          x[c] = x[c] * kTreeLog2e;
-          top = fmaxf(top, x[c] - M[c]);
-        }
-        if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, top > kRaise || !live)) {
-          if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, !live)) {
-            ok = false;
-            break;
-          }
-          // raise M to the largest logit so far, row by row
+        if (raise) {
+          // M becomes the largest logit so far, row by row
 #pragma unroll
           for (int c = 0; c < C; ++c) {
             float m = x[c];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) red[quarter * N + C * half + c] = m;
+            if (lane == 0) red[quarter * N + C * half + c] = m * kTreeLog2e;
           }
-          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+          if (!meeting()) break;
 #pragma unroll
           for (int c0 = 0; c0 < C; c0 += 8) {
             float f[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const int r = C * half + c0 + c;
-              const float m = fmaxf(fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])), M[c0 + c]);
-              f[c] = ex2(M[c0 + c] - m);
+              const float m = fmaxf(fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])), -nM[c0 + c]);
+              f[c] = ex2(-nM[c0 + c] - m);
               Z[c0 + c] *= f[c];
-              M[c0 + c] = m;
+              nM[c0 + c] = -m;
             }
             if (tile > un.t0) {
 #pragma unroll 1
@@ -531,18 +568,18 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             }
           }
           ptx::tmem_wait_st();
-          ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);   // `red` is free again
+          if (!meeting()) break;                               // `red` is free again
         }
+        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          x[c] = ex2(x[c] - M[c]);
-          Z[c] += x[c];
+        for (int c = 0; c < C; c += 2) {
+          ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(kTreeLog2e, kTreeLog2e), ptx::f32x2(nM[c], nM[c + 1])),
+                           x[c], x[c + 1]);
+          top = fmaxf(top, fmaxf(x[c], x[c + 1]));
         }
-        if (hurt) {
+        if (top > kRaise && !raise) *too_high = ev;
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-            if ((hurt >> c) & 1u) Z[c] = __int_as_float(0x7fc00000);
-        }
+        for (int c = 0; c < C; ++c) x[c] = ex2(x[c]);
 #pragma unroll
         for (int c = 0; c < C; c += 8)
           *reinterpret_cast<uint4*>(pt + (c / 8) * 2048) = make_uint4(pack2(x[c], x[c + 1]), pack2(x[c + 2], x[c + 3]),
@@ -551,8 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_full);
+        ++ev;
+        if (hurt) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if ((hurt >> c) & 1u) x[c] = __int_as_float(0x7fc00000);
+        }
       }
       if (!ok) break;
+      ++ev;
       // ---- the unit's sums
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -560,17 +604,12 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red[quarter * N + C * half + c] = z;
-        if (lane == 0 && quarter == 0) row_mz[C * half + c].x = M[c];
+        if (lane == 0 && quarter == 0) row_mz[C * half + c].x = -nM[c];
       }
-      const bool live = warp_wait(o_full, nu & 1, wt, 0xC32);
       if (sid == 0) *broken = 0ull;
-      if (ptx::named_bar_or(kBarSoftmax, 32 * kSoftmaxWarps, !live)) {
-        ok = false;
-        break;
-      }
-      ptx::tc_fence_after();
+      if (!meeting()) break;
       if (sid < N) row_mz[sid].y = (red[sid] + red[N + sid]) + (red[2 * N + sid] + red[3 * N + sid]);
-      ptx::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      if (!meeting()) break;
       const bool whole = un.parts == 1;
       const int64_t row0 = (int64_t)un.b * t.T * t.H + (int64_t)un.rb * N;
       if (whole ? p.lse && sid < rows : sid < rows && LCA_CHECK(t.err, u < p.slots, 0xD40)) {
