@@ -160,62 +160,78 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      int64_t nc = 0;
-      int ns = 0;
-      int64_t sent[kMaxSlots];
-#pragma unroll
-      for (int i = 0; i < kMaxSlots; ++i) sent[i] = 0;
-      bool ok = true;
-      Step s = st0;
-      int last_b = -1, last_tile = -1;
-      for (int64_t u = u0; u < u1 && ok; ++u, next(s)) {
-        const TreeLens l = tree_lens(t, s.b);
-        const int total = l.n + l.d, pos = s.tile * kTreeTile;
-        const int r0 = (int)tree_row(t, s.b, pos, 0xB06);
-        const int r1 = pos + 64 < total ? (int)tree_row(t, s.b, pos + 64, 0xB06) : r0;
-        const int qrow = (int)((int64_t)s.b * t.T * t.H + (int64_t)s.rb * N);
-        auto load_tile = [&](uint8_t* dst, int c, uint64_t* bar) {
-          const CUtensorMap* map = c < 8 ? &p.tm_c : &p.tm_k;
-          const int x = c < 8 ? 64 * c : 0;
-          ptx::tma_load_2d(dst, map, x, r0, bar);
-          ptx::tma_load_2d(dst + kChunk / 2, map, x, r1, bar);
-        };
-        auto load_q = [&](uint8_t* dst, int c, uint64_t* bar) {
-          ptx::tma_load_2d(dst, c < 8 ? &p.tm_qc : &p.tm_qr, c < 8 ? 64 * c : 0, qrow, bar);
-        };
-        if (s.b != last_b || (kStream && s.tile != last_tile)) {
-          last_b = s.b;
-          last_tile = s.tile;
-          if (ns > 0) ok = ttc::wait(stay_empty, (ns - 1) & 1, wt, 0xC40);
-          if (!ok) break;
+    // Converged, with one elected lane; a step's rows are looked up a step ahead.
+    int ns = 0, slot = 0, use = 0, sent = 0;
+    bool ok = true, skip = p.debug_skip_load != 0;
+    Step s = st0;
+    int last_b = -1, last_tile = -1;
+    int r0 = 0, r1 = 0;
+    auto rows_of = [&](const Step& x, int& a, int& b) {
+      const TreeLens l = tree_lens(t, x.b);
+      const int pos = x.tile * kTreeTile;
+      a = (int)tree_row(t, x.b, pos, 0xB06);
+      b = pos + 64 < l.n + l.d ? (int)tree_row(t, x.b, pos + 64, 0xB06) : a;
+    };
+    if (u0 < u1) rows_of(s, r0, r1);
+    for (int64_t u = u0; u < u1 && ok; ++u) {
+      const int b = s.b, tile = s.tile;
+      const int qrow = (int)((int64_t)s.b * t.T * t.H + (int64_t)s.rb * N);
+      int n0 = r0, n1 = r1;
+      next(s);
+      if (u + 1 < u1 && (s.b != b || s.tile != tile)) rows_of(s, n0, n1);
+      auto load_tile = [&](uint8_t* dst, int c, uint64_t* bar) {
+        const CUtensorMap* map = c < 8 ? &p.tm_c : &p.tm_k;
+        const int x = c < 8 ? 64 * c : 0;
+        ptx::tma_load_2d(dst, map, x, r0, bar);
+        ptx::tma_load_2d(dst + kChunk / 2, map, x, r1, bar);
+      };
+      auto load_q = [&](uint8_t* dst, int c, uint64_t* bar) {
+        ptx::tma_load_2d(dst, c < 8 ? &p.tm_qc : &p.tm_qr, c < 8 ? 64 * c : 0, qrow, bar);
+      };
+      if (b != last_b || (kStream && tile != last_tile)) {
+        last_b = b;
+        last_tile = tile;
+        if (ns > 0) ok = ttc::warp_wait(stay_empty, (ns - 1) & 1, wt, 0xC40);
+        if (!ok) break;
+        if (ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(stay_full, 9 * L::kStay);
+#pragma unroll
           for (int c = 0; c < 9; ++c) {
             if constexpr (kStream) load_tile(smem + c * L::kStay, c, stay_full);
             else load_q(smem + c * L::kStay, c, stay_full);
           }
-          ++ns;
         }
-        for (int c = 0; c < 9 && ok; ++c, ++nc) {
-          const int slot = (int)(nc % kSlots);
-          const int64_t use = nc / kSlots;
-          if (use > 0) ok = ttc::wait(empty + slot, (uint32_t)(use - 1) & 1, wt, 0xC41);
-          if (!ok) break;
-          if (p.debug_skip_load && nc == 0) continue;
+        __syncwarp();
+        ++ns;
+      }
+#pragma unroll
+      for (int c = 0; c < 9; ++c) {
+        if (use > 0) ok = ttc::warp_wait(empty + slot, (use - 1) & 1, wt, 0xC41);
+        if (!ok) break;
+        if (!skip && ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(full + slot, kChunk);
           uint8_t* dst = smem + L::kOffRing + slot * kChunk;
           if constexpr (kStream) load_q(dst, c, full + slot);
           else load_tile(dst, c, full + slot);
-#pragma unroll
-          for (int q = 0; q < kMaxSlots; ++q)
-            if (q == slot) sent[q] = use + 1;
+        }
+        __syncwarp();
+        if (!skip && use == 0) sent |= 1 << slot;
+        skip = false;
+        if (++slot == kSlots) {
+          slot = 0;
+          ++use;
         }
       }
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i)
-        if (sent[i] > 0) ttc::wait(full + i, (uint32_t)(sent[i] - 1) & 1, wt, 0xC4F, false);
-      if (ns > 0) ttc::wait(stay_full, (ns - 1) & 1, wt, 0xC4F, false);
+      r0 = n0;
+      r1 = n1;
     }
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const int fills = use + (i < slot ? 1 : 0);
+      if (fills > 1 || (fills == 1 && ((sent >> i) & 1))) ttc::wait(full + i, (fills - 1) & 1, wt, 0xC4F, false);
+    }
+    if (ns > 0) ttc::wait(stay_full, (ns - 1) & 1, wt, 0xC4F, false);
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
     // The whole warp runs this and one elected lane issues; the next chunk's barrier is probed

@@ -237,71 +237,85 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    int64_t np = 0;             // slots filled
-    int nk = 0, nq = 0;         // K tiles, query blocks
-    int64_t sent[kMaxSlots];    // loads into each slot (for the last wait)
-#pragma unroll
-    for (int i = 0; i < kMaxSlots; ++i) sent[i] = 0;
-    bool ok = true;
+    // Converged, with one elected lane, like the MMA warp; a tile's rows are looked up a tile ahead.
+    int nk = 0, nq = 0, slot = 0, use = 0;     // K tiles, query blocks; next slot, and how often each was filled
+    int sent = 0;                              // slots that were ever filled (for the last waits)
+    bool ok = true, skip = p.debug_skip_load != 0;
     for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
-      if (lane == 0) {
-        const TreeLens l = tree_lens(t, un.b);
-        const int total = l.n + l.d;
-        const int qrow = (int)((int64_t)un.b * t.T * t.H + (int64_t)un.rb * N);
-        if (nq > 0) ok = wait(q_empty, (nq - 1) & 1, wt, 0xC10);
-        if (ok) {
-          ptx::mbar_arrive_expect_tx(q_full, 9 * L::kQChunk);
-          for (int c = 0; c < 8; ++c) ptx::tma_load_2d(smem + L::kOffQ + c * L::kQChunk, &p.tm_qc, 64 * c, qrow, q_full);
-          ptx::tma_load_2d(smem + L::kOffQ + 8 * L::kQChunk, &p.tm_qr, 0, qrow, q_full);
-          ++nq;
-        }
-        for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
-          const int pos = tile * kTreeTile;
-          const int r0 = (int)tree_row(t, un.b, pos, 0xB05);
-          // a second half without tokens is loaded from the first half's rows, and zeroed later
-          const int r1 = pos + 64 < total ? (int)tree_row(t, un.b, pos + 64, 0xB05) : r0;
-          for (int i = 0; i < 5 && ok; ++i) {
-            if (i == kKAt) {
-              if (nk > 0) ok = wait(k_empty, (nk - 1) & 1, wt, 0xC11);
-              if (!ok) break;
+      const TreeLens l = tree_lens(t, un.b);
+      const int total = l.n + l.d;
+      // a tile's two halves of 64 rows; a second half without tokens is loaded from the first half's rows, and
+      // zeroed later
+      auto rows_of = [&](int tile, int& r0, int& r1) {
+        const int pos = tile * kTreeTile;
+        r0 = (int)tree_row(t, un.b, pos, 0xB05);
+        r1 = pos + 64 < total ? (int)tree_row(t, un.b, pos + 64, 0xB05) : r0;
+      };
+      int r0, r1, n0 = 0, n1 = 0;
+      rows_of(un.t0, r0, r1);
+      const int qrow = (int)((int64_t)un.b * t.T * t.H + (int64_t)un.rb * N);
+      if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10);
+      if (!ok) break;
+      if (ptx::elect_one()) {
+        ptx::mbar_arrive_expect_tx(q_full, 9 * L::kQChunk);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ptx::tma_load_2d(smem + L::kOffQ + c * L::kQChunk, &p.tm_qc, 64 * c, qrow, q_full);
+        ptx::tma_load_2d(smem + L::kOffQ + 8 * L::kQChunk, &p.tm_qr, 0, qrow, q_full);
+      }
+      __syncwarp();
+      ++nq;
+      for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
+        if (tile + 1 < un.t1) rows_of(tile + 1, n0, n1);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          if (i == kKAt) {
+            if (nk > 0) ok = warp_wait(k_empty, (nk - 1) & 1, wt, 0xC11);
+            if (!ok) break;
+            if (ptx::elect_one()) {
               ptx::mbar_arrive_expect_tx(k_full, kChunk);
               ptx::tma_load_2d(smem + L::kOffK, &p.tm_k, 0, r0, k_full);
               ptx::tma_load_2d(smem + L::kOffK + kChunk / 2, &p.tm_k, 0, r1, k_full);
-              ++nk;
-              continue;
             }
-            const int m = i < kKAt ? i : i - 1;
-            const int slot = (int)(np % kSlots);
-            const int64_t use = np / kSlots;
-            if (use > 0) ok = wait(empty + slot, (uint32_t)(use - 1) & 1, wt, 0xC12);
-            if (!ok) break;
-            if (!(p.debug_skip_load && np == 0)) {
-              ptx::mbar_arrive_expect_tx(full + slot, kSlot);
-              uint8_t* dst = smem + slot * kSlot;
+            __syncwarp();
+            ++nk;
+            continue;
+          }
+          const int m = i < kKAt ? i : i - 1;
+          const int at = kSlots == 4 ? m : slot;
+          if (use > 0) ok = warp_wait(empty + at, (use - 1) & 1, wt, 0xC12);
+          if (!ok) break;
+          if (!skip && ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(full + at, kSlot);
+            uint8_t* dst = smem + at * kSlot;
 #pragma unroll
-              for (int ch = 0; ch < 2; ++ch) {
-                ptx::tma_load_2d(dst + ch * kChunk, &p.tm_c, 128 * m + 64 * ch, r0, full + slot);
-                ptx::tma_load_2d(dst + ch * kChunk + kChunk / 2, &p.tm_c, 128 * m + 64 * ch, r1, full + slot);
-              }
-#pragma unroll
-              for (int q = 0; q < kMaxSlots; ++q)
-                if (q == slot) sent[q] = use + 1;
+            for (int ch = 0; ch < 2; ++ch) {
+              ptx::tma_load_2d(dst + ch * kChunk, &p.tm_c, 128 * m + 64 * ch, r0, full + at);
+              ptx::tma_load_2d(dst + ch * kChunk + kChunk / 2, &p.tm_c, 128 * m + 64 * ch, r1, full + at);
             }
-            ++np;
+          }
+          __syncwarp();
+          if (!skip && use == 0) sent |= 1 << at;
+          skip = false;
+          if (++slot == kSlots) {
+            slot = 0;
+            ++use;
           }
         }
+        r0 = n0;
+        r1 = n1;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (lane == 0) {            // every copy lands before the CTA may exit
+    // every copy lands before the CTA may exit: the last phase of each slot
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i)
-        if (sent[i] > 0) wait(full + i, (uint32_t)(sent[i] - 1) & 1, wt, 0xC1F, false);
-      if (nk > 0) wait(k_full, (nk - 1) & 1, wt, 0xC1F, false);
-      if (nq > 0) wait(q_full, (nq - 1) & 1, wt, 0xC1F, false);
+    for (int i = 0; i < kSlots; ++i) {
+      const int fills = use + (i < slot ? 1 : 0);
+      if (fills > 1 || (fills == 1 && ((sent >> i) & 1))) wait(full + i, (fills - 1) & 1, wt, 0xC1F, false);
     }
+    if (nk > 0) wait(k_full, (nk - 1) & 1, wt, 0xC1F, false);
+    if (nq > 0) wait(q_full, (nq - 1) & 1, wt, 0xC1F, false);
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
     constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, N, 0, 0);     // both K-major
