@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "tree_common.cuh"
 
 namespace lca {
@@ -15,9 +16,14 @@ namespace lca {
 // where sums are equal.  A sum that is not a number counts as the smallest.
 // All rows stay where n <= budget.  The kept rows are written in rising order.
 //
-// The sums map to unsigned keys of the same order; the key of the last row kept
-// is found 8 bits at a time (a histogram of the keys that share the bits found
-// so far), then one pass in row order writes the rows.
+// The sums map to unsigned keys of the same order.  A sequence belongs to a
+// cluster of CTAs, each with a contiguous run of its rows, whose keys it reads
+// once and keeps in shared memory.  The key of the last row kept is found 11, 11
+// and 10 bits at a time: a histogram per CTA of the keys that share the bits
+// found so far, added up over the cluster by every CTA for itself.  Then each
+// warp counts the kept rows of its run, the counts before it (its CTA's, and
+// the lower CTAs' totals) say where its rows go, and it writes them in order.
+// What bounds it is latency: five cluster barriers and three histograms.
 struct SelectParams {
   const float* scores;          // [B][stride]
   int64_t stride;
@@ -28,6 +34,7 @@ struct SelectParams {
   int budget;                   // entries a row of `kept` has
   int32_t* kept;                // [B][budget]
   int32_t* kept_lens;           // [B]
+  int ctas;                     // of a cluster, which takes one sequence
   int* err;
 };
 
@@ -38,103 +45,193 @@ __device__ __forceinline__ uint32_t select_key(float x) {
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectBins = 2048;
+constexpr int kSelectKeep = 40960;          // keys of a CTA in shared memory; later ones are read again
+constexpr int kSelectMaxCtas = 8;
+
+__host__ __device__ inline size_t select_smem(int64_t run) {
+  const int64_t keys = run < kSelectKeep ? run : kSelectKeep;
+  return sizeof(int) * (3 * kSelectBins + (size_t)keys);
+}
+
+// Rows a CTA of `ctas` takes of n: a multiple of 32 x warps, so that every warp's run starts on a 128-byte line.
+__host__ __device__ inline int64_t select_run(int64_t n, int ctas) {
+  const int64_t per = (n + ctas - 1) / ctas;
+  return (per + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+}
+
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::mapa(ptx::smem_u32(p), rank)) : "memory");
+  return v;
+}
 
 __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const SelectParams p) {
-  __shared__ int hist[256];
+  extern __shared__ int select_dyn[];
+  int* hist = select_dyn;                                       // [3][2048]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(select_dyn + 3 * kSelectBins);
+  __shared__ int warp_sum[kSelectWarps], warp_eq[kSelectWarps];
   __shared__ int s_bin, s_above;
-  __shared__ int wk[kSelectThreads / 32], we[kSelectThreads / 32];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int totals[2];                                     // rows kept for sure, rows of the last key
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = p.ctas, rank = blockIdx.x % ctas, b = blockIdx.x / ctas;
   const int n = p.seq_lens[b];
+  int32_t* kept = p.kept + (int64_t)b * p.budget;
   if (n < 0 || n > p.cap) {
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
       input_error(p.err, 0xB10);
       p.kept_lens[b] = 0;
     }
     return;
   }
-  const float* x = p.scores + (int64_t)b * p.stride;
-  int32_t* kept = p.kept + (int64_t)b * p.budget;
-  if (tid == 0) p.kept_lens[b] = min(n, p.budget);
+  if (rank == 0 && tid == 0) p.kept_lens[b] = min(n, p.budget);
   if (n <= p.budget) {
-    for (int i = tid; i < n; i += kSelectThreads) kept[i] = i;
+    for (int i = rank * kSelectThreads + tid; i < n; i += ctas * kSelectThreads) kept[i] = i;
     return;
   }
-  const int lo = p.n_sink, hi = n - p.n_recent;
-  int need = p.budget - p.n_sink - p.n_recent;                  // rows to take from [lo, hi)
-  uint32_t prefix = 0, have = 0;                                // key bits found; their mask
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+  const float* x = p.scores + (int64_t)b * p.stride;
+  const int run = (int)select_run(n, ctas);                     // this CTA: rows [r0, r1)
+  const int r0 = (int)min((int64_t)n, (int64_t)rank * run), r1 = min(n, r0 + run);
+  const int lo = p.n_sink, hi = n - p.n_recent;                 // rows that compete
+  auto key_of = [&](int i) { return i - r0 < kSelectKeep ? keys[i - r0] : select_key(x[i]); };
+  for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) hist[i] = 0;
+  __syncthreads();
+  int need = p.budget - p.n_sink - p.n_recent;                  // rows to take of [lo, hi)
+  const bool any = need > 0;
+  uint32_t prefix = 0, have = 0;                                // bits of the last key found; their mask
+  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    int* h = hist + pass * kSelectBins;
+    constexpr int kUnroll = 8;
+    for (int i0 = r0; i0 < r1; i0 += kUnroll * kSelectThreads) {
+      uint32_t k[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kSelectThreads + tid;
+        k[u] = 0;
+        if (i < r1) k[u] = pass == 0 ? select_key(x[i]) : key_of(i);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kSelectThreads + tid;
+        if (i >= r1) continue;
+        if (pass == 0 && i - r0 < kSelectKeep) keys[i - r0] = k[u];
+        if (i >= lo && i < hi && (k[u] & have) == prefix) atomicAdd(&h[(k[u] >> kShift[pass]) & ((1u << kBits[pass]) - 1u)], 1);
+      }
+    }
+    ptx::cluster_sync();                                        // (also the CTA's own barrier)
+    if (any) {
+      // bins from the top: thread t has bins 2047 - 2t and 2046 - 2t
+      const int b1 = kSelectBins - 1 - 2 * tid, b0 = b1 - 1;
+      int c1 = 0, c0 = 0;
+      for (int r = 0; r < ctas; ++r) {
+        c1 += ld_cluster(h + b1, r);
+        c0 += ld_cluster(h + b0, r);
+      }
+      int incl = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelectThreads) {
-        const uint32_t k = select_key(x[i]);
-        if ((k & have) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += warp_sum[w];
+      const int above1 = before + incl - c0 - c1, above0 = above1 + c1;   // rows in higher bins
+      if (above1 < need && need <= above1 + c1) {
+        s_bin = b1;
+        s_above = above1;
+      }
+      if (above0 < need && need <= above0 + c0) {
+        s_bin = b0;
+        s_above = above0;
       }
       __syncthreads();
-      if (tid == 0) {
-        int above = 0, bin = 255;
-        for (; bin > 0; --bin) {
-          if (above + hist[bin] >= need) break;
-          above += hist[bin];
-        }
-        s_bin = bin;
-        s_above = above;
-      }
-      __syncthreads();
-      prefix |= (uint32_t)s_bin << shift;
-      have |= 255u << shift;
+      prefix |= (uint32_t)s_bin << kShift[pass];
+      have |= ((1u << kBits[pass]) - 1u) << kShift[pass];
       need -= s_above;
-      __syncthreads();
     }
   }
-  // rows in order: kept by place, by a larger key, or among the first `need` of the equal ones
-  const bool any = p.budget - p.n_sink - p.n_recent > 0;
-  int done = 0, equal = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    bool keep = false, eq = false;
-    if (i < n) {
-      if (i < lo || i >= hi) {
-        keep = true;
-      } else if (any) {
-        const uint32_t k = select_key(x[i]);
-        keep = k > prefix;
-        eq = k == prefix;
-      }
+  // a warp's rows: kept for sure (by place, or by a larger key), or of the last key
+  const int per_warp = run / kSelectWarps;
+  const int w0 = min(r1, r0 + warp * per_warp), w1 = min(r1, w0 + per_warp);
+  auto judge = [&](int i, bool& sure, bool& eq) {
+    sure = eq = false;
+    if (i >= w1) return;
+    if (i < lo || i >= hi) {
+      sure = true;
+    } else if (any) {
+      const uint32_t k = key_of(i);
+      sure = k > prefix;
+      eq = k == prefix;
     }
-    const uint32_t eb = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) we[warp] = __popc(eb);
-    __syncthreads();
-    int before = equal, all = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-      if (w < warp) before += we[w];
-      all += we[w];
-    }
-    if (eq) keep = before + __popc(eb & ((1u << lane) - 1u)) < need;
-    equal += all;
-    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) wk[warp] = __popc(kb);
-    __syncthreads();
-    int at = done, sum = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-      if (w < warp) at += wk[w];
-      sum += wk[w];
-    }
-    if (keep) kept[at + __popc(kb & ((1u << lane) - 1u))] = i;
-    done += sum;
-    __syncthreads();
+  };
+  int n_sure = 0, n_eq = 0;
+  for (int i = w0 + lane; __any_sync(0xffffffffu, i < w1); i += 32) {
+    bool sure, eq;
+    judge(i, sure, eq);
+    n_sure += __popc(__ballot_sync(0xffffffffu, sure));
+    n_eq += __popc(__ballot_sync(0xffffffffu, eq));
   }
+  if (lane == 0) {
+    warp_sum[warp] = n_sure;
+    warp_eq[warp] = n_eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sum[lane], e = warp_eq[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    if (lane == 0) {
+      totals[0] = s;
+      totals[1] = e;
+    }
+  }
+  ptx::cluster_sync();
+  int sure_before = 0, eq_before = 0;
+  for (int r = 0; r < rank; ++r) {
+    sure_before += ld_cluster(totals, r);
+    eq_before += ld_cluster(totals + 1, r);
+  }
+  for (int w = 0; w < warp; ++w) {
+    sure_before += warp_sum[w];
+    eq_before += warp_eq[w];
+  }
+  for (int i = w0 + lane; __any_sync(0xffffffffu, i < w1); i += 32) {
+    bool sure, eq;
+    judge(i, sure, eq);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t sb = __ballot_sync(0xffffffffu, sure), eb = __ballot_sync(0xffffffffu, eq);
+    // of the rows with the last key the first `need` stay
+    const int eq_rank = eq_before + __popc(eb & below);
+    const int at = sure_before + __popc(sb & below) + min(eq_rank, need);
+    if (sure || (eq && eq_rank < need)) kept[at] = i;
+    sure_before += __popc(sb);
+    eq_before += __popc(eb);
+  }
+  ptx::cluster_sync();                                          // no CTA leaves while its counts may be read
 }
 
 // ---------------------------------------------------------------- moving rows
 // Row dst0 + j of a sequence becomes its row src[j], j = 0 .. m - 1, in place;
-// src rises strictly and src[j] >= dst0 + j.  A block moves one 16-byte-wide
-// strip of columns (or a few) of one sequence, tile after tile of rows in
-// order: the rows of a tile are read into registers by the whole block before
-// any of them is written, and every later tile reads only rows above those
-// written so far (src[j] >= dst0 + j), so no row is overwritten before it is
-// read; different strips do not meet.  Rows at their place already (src[j] =
-// dst0 + j, the first ones, since src[j] - j never falls) are passed over.
+// src rises strictly and src[j] >= dst0 + j.  A block moves one strip of columns
+// (2, 4 or 8 times 16 bytes) of one sequence, tile after tile of rows in order.
+// No row is overwritten before it is read: the rows of a tile are in registers
+// of the whole block before any of them is written, later tiles read only rows
+// above all those written so far (src[j] >= dst0 + j), and strips do not meet.
+// For the same reason the next tile's reads may be under way while this tile is
+// written, so two tiles (16 reads of 16 bytes a thread) are in flight.
+//
+// It is bound by memory latency and then bandwidth: a strip is as wide as
+// leaves about one block per SM (narrower ones cost DRAM and L2 efficiency, wider
+// ones leave SMs idle).  Rows at their place already (src[j] = dst0 + j, the
+// first ones, since src[j] - j never falls) are passed over.
 struct CompactParams {
   TreeBatch t;                  // the cache; lengths and masks unused
   int elem;                     // bytes of an element
@@ -162,10 +259,11 @@ __device__ __forceinline__ int64_t compact_row(const TreeBatch& t, int b, int po
 
 constexpr int kCompactThreads = 256;
 constexpr int kCompactUnroll = 8;
+constexpr int kCompactMaxStrip = 8, kCompactMinStrip = 2;
 
 __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const CompactParams p) {
   const TreeBatch& t = p.t;
-  const int b = blockIdx.y, tid = threadIdx.x;
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int m = p.n_src[b];
   const int d0 = p.dst0 ? p.dst0[b] : 0;
   if (m < 0 || m > p.src_stride || d0 < 0 || (int64_t)d0 + m > t.cap) {
@@ -173,34 +271,36 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
     return;
   }
   const int32_t* src = p.src + (int64_t)b * p.src_stride;
+  // rows at their place: the first j with src[j] != dst0 + j, 32 probes at a time
   int first = 0;
-  for (int hi = m; first < hi;) {
-    const int mid = (first + hi) >> 1;
-    if (src[mid] == d0 + mid) first = mid + 1; else hi = mid;
+  for (int span = m; span > 0;) {
+    const int step = (span + 31) / 32, j = first + lane * step;
+    const bool moved = j >= first + span || src[j] != d0 + j;
+    const uint32_t vote = __ballot_sync(0xffffffffu, moved);
+    const int hit = vote ? __ffs(vote) - 1 : 32;               // probes before it are at their place
+    if (hit == 0) break;
+    const int end = first + span;
+    first += (hit - 1) * step + 1;
+    span = min(step - 1, end - first);
   }
+  // row j of the list: where it is and where it goes; -1 where it stays put
+  auto check = [&](int j, int& s) {
+    s = src[j];
+    const bool ok = s >= d0 + j && s < t.cap && (j == 0 || s > src[j - 1]);
+    if (!ok) input_error(t.err, 0xB21);
+    return ok;
+  };
   int sx = blockIdx.x;
-  uint8_t* base;
-  int row_bytes, col, cols;     // this block's columns: [col, col + cols) of 16 bytes
-  const bool is_score = sx >= p.strips_c + p.strips_k;
-  if (sx < p.strips_c) {
-    base = static_cast<uint8_t*>(const_cast<void*>(t.c));
-    row_bytes = t.d_c * p.elem;
-  } else {
-    sx -= p.strips_c;
-    base = static_cast<uint8_t*>(const_cast<void*>(t.k));
-    row_bytes = t.d_r * p.elem;
-  }
-  if (is_score) {
+  if (sx >= p.strips_c + p.strips_k) {
+    float* sc = p.scores + (int64_t)b * p.score_stride;
     for (int j0 = first; j0 < m; j0 += kCompactThreads * kCompactUnroll) {
       float v[kCompactUnroll];
       bool ok[kCompactUnroll];
-      float* sc = p.scores + (int64_t)b * p.score_stride;
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int j = j0 + u * kCompactThreads + tid;
-        const int s = j < m ? src[j] : 0;
-        ok[u] = j < m && s >= d0 + j && s < t.cap && (j == 0 || s > src[j - 1]);
-        if (j < m && !ok[u]) input_error(t.err, 0xB21);
+        int s = 0;
+        ok[u] = j < m && check(j, s);
         v[u] = ok[u] ? sc[s] : 0.f;
       }
       __syncthreads();
@@ -211,29 +311,63 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
     }
     return;
   }
-  col = sx * p.strip;
-  cols = min(p.strip, row_bytes / 16 - col);
-  const int rows_step = kCompactThreads / p.strip;
+  uint8_t* base;
+  int row_bytes;
+  if (sx < p.strips_c) {
+    base = static_cast<uint8_t*>(const_cast<void*>(t.c));
+    row_bytes = t.d_c * p.elem;
+  } else {
+    sx -= p.strips_c;
+    base = static_cast<uint8_t*>(const_cast<void*>(t.k));
+    row_bytes = t.d_r * p.elem;
+  }
+  constexpr int kMaxRows = kCompactThreads / kCompactMinStrip * kCompactUnroll;
+  __shared__ int from_s[2][kMaxRows], to_s[2][kMaxRows];        // pool rows of a tile
+  const int step = kCompactThreads / p.strip;                   // rows a block reads at once
+  const int rows = step * kCompactUnroll;                       // of a tile
   const int x = tid % p.strip, y = tid / p.strip;
-  const bool act = x < cols && y < rows_step;
-  for (int j0 = first; j0 < m; j0 += rows_step * kCompactUnroll) {
-    uint4 v[kCompactUnroll];
-    int64_t to[kCompactUnroll];             // where the row goes; -1: nowhere
+  const bool act = x < row_bytes / 16 - sx * p.strip;
+  base += (sx * p.strip + x) * 16;
+  auto look_up = [&](int j0, int buf) {
+    for (int i = tid; i < rows; i += kCompactThreads) {
+      const int j = j0 + i;
+      int64_t from = -1, to = -1;
+      int s;
+      if (j < m && check(j, s)) {
+        from = compact_row(t, b, s);
+        to = from < 0 ? -1 : compact_row(t, b, d0 + j);
+      }
+      from_s[buf][i] = (int)from;
+      to_s[buf][i] = (int)to;
+    }
+  };
+  uint4 v[kCompactUnroll], w[kCompactUnroll];
+  int to[kCompactUnroll], to_w[kCompactUnroll];
+  auto read = [&](int buf, uint4 (&d)[kCompactUnroll], int (&g)[kCompactUnroll]) {
 #pragma unroll
     for (int u = 0; u < kCompactUnroll; ++u) {
-      const int j = j0 + u * rows_step + y;
-      const int s = act && j < m ? src[j] : 0;
-      const bool ok = act && j < m && s >= d0 + j && s < t.cap && (j == 0 || s > src[j - 1]);
-      if (act && j < m && !ok) input_error(t.err, 0xB21);
-      const int64_t from = ok ? compact_row(t, b, s) : -1;
-      to[u] = from >= 0 ? compact_row(t, b, d0 + j) : -1;
-      if (to[u] >= 0) v[u] = *reinterpret_cast<const uint4*>(base + from * row_bytes + (col + x) * 16);
+      const int i = u * step + y;
+      g[u] = act ? to_s[buf][i] : -1;
+      if (g[u] >= 0) d[u] = *reinterpret_cast<const uint4*>(base + (int64_t)from_s[buf][i] * row_bytes);
     }
-    __syncthreads();
+  };
+  look_up(first, 0);
+  __syncthreads();
+  read(0, v, to);
+  int buf = 0;
+  for (int j0 = first; j0 < m; j0 += rows) {
+    buf ^= 1;
+    look_up(j0 + rows, buf);
+    __syncthreads();            // this tile's rows are read, the next one's are looked up
+    read(buf, w, to_w);
 #pragma unroll
     for (int u = 0; u < kCompactUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u] * row_bytes + (col + x) * 16) = v[u];
-    __syncthreads();
+      if (to[u] >= 0) *reinterpret_cast<uint4*>(base + (int64_t)to[u] * row_bytes) = v[u];
+#pragma unroll
+    for (int u = 0; u < kCompactUnroll; ++u) {
+      v[u] = w[u];
+      to[u] = to_w[u];
+    }
   }
 }
 

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -107,9 +108,16 @@ lca_status check_batch(const lca_plan* p, int n_draft, const int32_t* seq_lens, 
   return LCA_OK;
 }
 
-template <typename K>
-bool allow_smem(K kernel, size_t smem) {
-  return smem <= 48 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+// Let a kernel have up to `most` bytes of shared memory, once per device (so that no call lowers what another
+// one, in another thread, is about to launch with).
+template <auto kKernel>
+bool allow_smem(int device, size_t most) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = device >= 0 && device < 64 ? uint64_t(1) << device : 0;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_acq_rel);
+  return true;
 }
 
 lca_status launched() { return cudaGetLastError() == cudaSuccess ? LCA_OK : LCA_ERR_CUDA; }
@@ -145,7 +153,7 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   sp.lse = lse;
   const size_t smem = lca::tree_simt_smem(t.d_c, t.d_r);
   if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
-  if (!allow_smem(lca::lca_tree_simt_kernel<T>, smem)) return LCA_ERR_CUDA;
+  if (!allow_smem<lca::lca_tree_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
   const dim3 grid((unsigned)sp.n_split, (unsigned)ceil_div((int64_t)t.T * t.H, lca::kTreeSimtRows), (unsigned)t.B);
   lca::lca_tree_simt_kernel<T><<<grid, lca::kTreeSimtThreads, smem, stream>>>(sp);
   const lca_status st = launched();
@@ -182,7 +190,7 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
   tp.lse = lse;
   tp.timeout_ns = p->timeout_ns;
   tp.debug_skip_load = p->debug_skip_load;
-  if (!allow_smem(ttc::lca_tree_tc_kernel<N>, ttc::Layout<N>::kAlloc)) return LCA_ERR_CUDA;
+  if (!allow_smem<ttc::lca_tree_tc_kernel<N>>(p->device, ttc::Layout<N>::kAlloc)) return LCA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tp.G, 1, 1);
   cfg.blockDim = dim3(ttc::kThreads, 1, 1);
@@ -210,7 +218,7 @@ template <typename T>
 lca_status run_mass_simt(const lca_plan* p, const lca::MassParams& mp, cudaStream_t stream) {
   const size_t smem = lca::tree_simt_smem(mp.t.d_c, mp.t.d_r);
   if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
-  if (!allow_smem(lca::lca_mass_simt_kernel<T>, smem)) return LCA_ERR_CUDA;
+  if (!allow_smem<lca::lca_mass_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
   const int64_t blocks = std::min<int64_t>(ceil_div(mp.t.cap, lca::kTreeSimtTile), std::max<int64_t>(1, 8LL * p->num_sms / p->B));
   lca::lca_mass_simt_kernel<T><<<dim3((unsigned)blocks, (unsigned)p->B), lca::kTreeSimtThreads, smem, stream>>>(mp);
   return launched();
@@ -235,7 +243,7 @@ lca_status run_mass_tc(const lca_plan* p, const lca::MassParams& m, uint8_t* ws,
   mp.part = reinterpret_cast<float*>(ws + w.o);
   mp.timeout_ns = p->timeout_ns;
   mp.debug_skip_load = p->debug_skip_load;
-  if (!allow_smem(mtc::lca_mass_tc_kernel<N, kStream>, mtc::Layout<N, kStream>::kAlloc)) return LCA_ERR_CUDA;
+  if (!allow_smem<mtc::lca_mass_tc_kernel<N, kStream>>(p->device, mtc::Layout<N, kStream>::kAlloc)) return LCA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)mp.G, 1, 1);
   cfg.blockDim = dim3(mtc::kThreads, 1, 1);
@@ -361,8 +369,25 @@ lca_status lca_evict_select(lca_plan* p, const float* scores, int64_t score_stri
   sp.kept = kept;
   sp.kept_lens = kept_lens;
   sp.err = p->err;
-  lca::lca_select_kernel<<<p->B, lca::kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(sp);
-  return launched();
+  // One CTA for up to 4096 rows, twice as many for twice the rows, up to a cluster of 8.
+  sp.ctas = 1;
+  while (sp.ctas < lca::kSelectMaxCtas && sp.cap > 4096LL * sp.ctas) sp.ctas *= 2;
+  if (p->B > INT32_MAX / lca::kSelectMaxCtas) return LCA_ERR_UNSUPPORTED;
+  const size_t smem = lca::select_smem(lca::select_run(sp.cap, sp.ctas));
+  if (!allow_smem<lca::lca_select_kernel>(p->device, lca::select_smem(lca::kSelectKeep))) return LCA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p->B * sp.ctas), 1, 1);
+  cfg.blockDim = dim3(lca::kSelectThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)sp.ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lca::lca_select_kernel, sp) == cudaSuccess ? LCA_OK : LCA_ERR_CUDA;
 }
 
 lca_status lca_cache_compact(lca_plan* p, void* c_pool, void* k_pool, int64_t num_pages, int page_size,
@@ -386,7 +411,10 @@ lca_status lca_cache_compact(lca_plan* p, void* c_pool, void* k_pool, int64_t nu
   cp.dst0 = dst0;
   cp.scores = scores;
   cp.score_stride = score_stride;
-  cp.strip = 8;
+  // the widest strip that still makes a block for each SM
+  const int64_t cols = (int64_t)(p->d_c + p->d_r) * cp.elem / 16;
+  cp.strip = lca::kCompactMaxStrip;
+  while (cp.strip > lca::kCompactMinStrip && p->B * cols / cp.strip < p->num_sms) cp.strip /= 2;
   cp.strips_c = (int)ceil_div((int64_t)p->d_c * cp.elem / 16, cp.strip);
   cp.strips_k = (int)ceil_div((int64_t)p->d_r * cp.elem / 16, cp.strip);
   const dim3 grid((unsigned)(cp.strips_c + cp.strips_k + (scores ? 1 : 0)), (unsigned)p->B);
