@@ -67,6 +67,22 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ int4 ld_cluster4(const int* p, uint32_t rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(ptx::mapa(ptx::smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+// The sum of the warps' values below `warp`.
+__device__ __forceinline__ int warp_prefix(const int* sums, int warp, int lane) {
+  int v = lane < warp ? sums[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const SelectParams p) {
   extern __shared__ int select_dyn[];
   int* hist = select_dyn;                                       // [3][2048]
@@ -104,7 +120,7 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     int* h = hist + pass * kSelectBins;
-    constexpr int kUnroll = 8;
+    constexpr int kUnroll = 16;
     for (int i0 = r0; i0 < r1; i0 += kUnroll * kSelectThreads) {
       uint32_t k[kUnroll];
 #pragma unroll
@@ -123,14 +139,20 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
     }
     ptx::cluster_sync();                                        // (also the CTA's own barrier)
     if (any) {
-      // bins from the top: thread t has bins 2047 - 2t and 2046 - 2t
-      const int b1 = kSelectBins - 1 - 2 * tid, b0 = b1 - 1;
-      int c1 = 0, c0 = 0;
-      for (int r = 0; r < ctas; ++r) {
-        c1 += ld_cluster(h + b1, r);
-        c0 += ld_cluster(h + b0, r);
+      // thread t < 512 has the four bins from 2047 - 4t down; their counts over the cluster, scanned from the top
+      int4 c = make_int4(0, 0, 0, 0);                           // .w the highest bin
+      const int bin0 = kSelectBins - 4 - 4 * tid;
+      if (tid < kSelectBins / 4) {
+        int4 v[kSelectMaxCtas];
+#pragma unroll
+        for (int r = 0; r < kSelectMaxCtas; ++r) v[r] = r < ctas ? ld_cluster4(h + bin0, r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kSelectMaxCtas; ++r) {
+          c.x += v[r].x; c.y += v[r].y; c.z += v[r].z; c.w += v[r].w;
+        }
       }
-      int incl = c0 + c1;
+      int incl = c.x + c.y + c.z + c.w;
+      const int mine = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -138,16 +160,15 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
       }
       if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
-      int before = 0;
-      for (int w = 0; w < warp; ++w) before += warp_sum[w];
-      const int above1 = before + incl - c0 - c1, above0 = above1 + c1;   // rows in higher bins
-      if (above1 < need && need <= above1 + c1) {
-        s_bin = b1;
-        s_above = above1;
-      }
-      if (above0 < need && need <= above0 + c0) {
-        s_bin = b0;
-        s_above = above0;
+      int above = warp_prefix(warp_sum, warp, lane) + incl - mine;      // rows in higher bins
+      const int count[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (above < need && need <= above + count[q]) {
+          s_bin = bin0 + 3 - q;
+          s_above = above;
+        }
+        above += count[q];
       }
       __syncthreads();
       prefix |= (uint32_t)s_bin << kShift[pass];
@@ -169,12 +190,20 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
       eq = k == prefix;
     }
   };
+  // lane j keeps the votes on the warp's j-th 32 rows (a warp of more than 1024 rows votes twice)
+  const bool votes_kept = per_warp <= 1024;
+  uint32_t my_sure = 0, my_eq = 0;
   int n_sure = 0, n_eq = 0;
-  for (int i = w0 + lane; __any_sync(0xffffffffu, i < w1); i += 32) {
+  for (int i0 = w0, j = 0; i0 < w1; i0 += 32, ++j) {
     bool sure, eq;
-    judge(i, sure, eq);
-    n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-    n_eq += __popc(__ballot_sync(0xffffffffu, eq));
+    judge(i0 + lane, sure, eq);
+    const uint32_t sb = __ballot_sync(0xffffffffu, sure), eb = __ballot_sync(0xffffffffu, eq);
+    if (lane == j) {
+      my_sure = sb;
+      my_eq = eb;
+    }
+    n_sure += __popc(sb);
+    n_eq += __popc(eb);
   }
   if (lane == 0) {
     warp_sum[warp] = n_sure;
@@ -194,24 +223,29 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
     }
   }
   ptx::cluster_sync();
-  int sure_before = 0, eq_before = 0;
-  for (int r = 0; r < rank; ++r) {
-    sure_before += ld_cluster(totals, r);
-    eq_before += ld_cluster(totals + 1, r);
-  }
-  for (int w = 0; w < warp; ++w) {
-    sure_before += warp_sum[w];
-    eq_before += warp_eq[w];
-  }
-  for (int i = w0 + lane; __any_sync(0xffffffffu, i < w1); i += 32) {
-    bool sure, eq;
-    judge(i, sure, eq);
+  int sure_before = warp_prefix(warp_sum, warp, lane), eq_before = warp_prefix(warp_eq, warp, lane);
+#pragma unroll
+  for (int r = 0; r < kSelectMaxCtas - 1; ++r)
+    if (r < rank) {
+      sure_before += ld_cluster(totals, r);
+      eq_before += ld_cluster(totals + 1, r);
+    }
+  for (int i0 = w0, j = 0; i0 < w1; i0 += 32, ++j) {
+    uint32_t sb, eb;
+    if (votes_kept) {
+      sb = __shfl_sync(0xffffffffu, my_sure, j);
+      eb = __shfl_sync(0xffffffffu, my_eq, j);
+    } else {
+      bool sure, eq;
+      judge(i0 + lane, sure, eq);
+      sb = __ballot_sync(0xffffffffu, sure);
+      eb = __ballot_sync(0xffffffffu, eq);
+    }
     const uint32_t below = (1u << lane) - 1u;
-    const uint32_t sb = __ballot_sync(0xffffffffu, sure), eb = __ballot_sync(0xffffffffu, eq);
     // of the rows with the last key the first `need` stay
     const int eq_rank = eq_before + __popc(eb & below);
     const int at = sure_before + __popc(sb & below) + min(eq_rank, need);
-    if (sure || (eq && eq_rank < need)) kept[at] = i;
+    if (((sb >> lane) & 1u) || (((eb >> lane) & 1u) && eq_rank < need)) kept[at] = i0 + lane;
     sure_before += __popc(sb);
     eq_before += __popc(eb);
   }

@@ -41,7 +41,8 @@ struct Workspace {
 // over B and the blocks of 8 rows; one part writes its output itself.
 int64_t simt_parts(const lca_plan* p, int T) {
   const int64_t units = (int64_t)p->B * ceil_div((int64_t)T * p->H, lca::kTreeSimtRows);
-  return std::max<int64_t>(1, std::min<int64_t>(4LL * p->num_sms / units, ceil_div(p->max_L, lca::kTreeSimtTile)));
+  const int64_t most = std::min<int64_t>(lca::kTreeMaxParts, ceil_div(p->max_L, lca::kTreeSimtTile));
+  return std::max<int64_t>(1, std::min<int64_t>(4LL * p->num_sms / units, most));
 }
 
 // The tensor-core kernels' shape.
@@ -124,10 +125,10 @@ lca_status launched() { return cudaGetLastError() == cudaSuccess ? LCA_OK : LCA_
 
 // The merge of the parts, a programmatic dependent of the kernel that wrote them.
 template <typename T>
-lca_status launch_merge(const lca::TreeMergeParams& mp, cudaStream_t stream) {
+lca_status launch_merge(const lca_plan* p, const lca::TreeMergeParams& mp, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const int64_t R = (int64_t)mp.t.T * mp.t.H;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(R, 65535), (unsigned)mp.t.B, 1);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(R, ceil_div(16LL * p->num_sms, mp.t.B)), (unsigned)mp.t.B, 1);
   cfg.blockDim = dim3(lca::kTreeMergeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -167,7 +168,7 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   mp.direct = sp.n_split == 1;
   mp.out = out;
   mp.lse = lse;
-  return launch_merge<T>(mp, stream);
+  return launch_merge<T>(p, mp, stream);
 }
 
 template <int N>
@@ -181,7 +182,7 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
       !lca::make_map(&tp.tm_qc, q_c, ttc::kDC, qrows, N) || !lca::make_map(&tp.tm_qr, q_r, ttc::kDR, qrows, N))
     return LCA_ERR_CUDA;
   tp.t = t;
-  tp.G = p->num_ctas > 0 ? p->num_ctas : p->num_sms;
+  tp.G = std::min(p->num_ctas > 0 ? p->num_ctas : p->num_sms, lca::kTreeMaxParts / lca::kTreeMaxWaves);
   tp.split = reinterpret_cast<lca::TreeSplit*>(ws);
   tp.part_mz = reinterpret_cast<float*>(ws + w.mz);
   tp.part_o = reinterpret_cast<float*>(ws + w.o);
@@ -211,7 +212,7 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
   mp.direct = true;
   mp.out = out;
   mp.lse = lse;
-  return launch_merge<__nv_bfloat16>(mp, stream);
+  return launch_merge<__nv_bfloat16>(p, mp, stream);
 }
 
 template <typename T>

@@ -78,6 +78,12 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // ---------------------------------------------------------------- merge of partial softmax sums
 // Row r = (node, head) of sequence b has n_part(b) partials (M, Z, O = sum
 // e^{x - M} c), M and Z in units of log2; they merge to
@@ -108,43 +114,84 @@ struct TreeMergeParams {
 };
 
 constexpr int kTreeMergeThreads = 128;
+constexpr int kTreeMaxParts = 1024;
 
 // One CTA per (node, head) row of one sequence; the parts are added in order.
+// Latency is what it costs: every part's (M, Z) is read at once by a thread of
+// its own, and a thread's four dims come from eight parts at a time.
 template <typename T>
 __global__ void __launch_bounds__(kTreeMergeThreads) lca_tree_merge_kernel(const TreeMergeParams p) {
+  __shared__ float weight[kTreeMaxParts];
+  __shared__ float2 warp_mz[kTreeMergeThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.y;
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const TreeSplit sp = p.split[b];
+  if (!sp.bad && (sp.parts == 0 || (p.direct && sp.parts == 1))) return;
   const TreeLens ln = tree_lens(p.t, b);
-  const int64_t R = (int64_t)p.t.T * p.t.H;
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+  const int64_t R = (int64_t)p.t.T * p.t.H, live = sp.bad ? R : (int64_t)ln.d * p.t.H;
+  const int quads = p.t.d_c / 4;
+  for (int64_t r = blockIdx.x; r < live; r += gridDim.x) {
     T* out = static_cast<T*>(p.out) + ((int64_t)b * R + r) * p.t.d_c;
     float* lse = p.lse ? p.lse + (int64_t)b * R + r : nullptr;
     if (sp.bad) {
-      for (int d = threadIdx.x; d < p.t.d_c; d += kTreeMergeThreads) out[d] = from_f32<T>(__int_as_float(0x7fc00000));
-      if (lse && threadIdx.x == 0) *lse = __int_as_float(0x7fc00000);
+      for (int d = tid; d < p.t.d_c; d += kTreeMergeThreads) out[d] = from_f32<T>(__int_as_float(0x7fc00000));
+      if (lse && tid == 0) *lse = __int_as_float(0x7fc00000);
       continue;
     }
-    if (r >= (int64_t)ln.d * p.t.H || (p.direct && sp.parts == 1)) continue;
     const int rb = (int)(r / p.rows_per_block), col = (int)(r - (int64_t)rb * p.rows_per_block);
+    const int64_t i0 = (int64_t)(sp.base + rb) * p.rows_per_block + col;     // the row in part 0's slot
+    const int64_t step = (int64_t)sp.rb * p.rows_per_block;
+    // M and Z over the parts: each thread its own, then the block's
     float M = -INFINITY, Z = 0.f;
-    for (int s = 0; s < sp.parts; ++s) {
-      const int64_t i = (int64_t)(sp.base + s * sp.rb + rb) * p.rows_per_block + col;
-      const float m = p.part_mz[2 * i], z = p.part_mz[2 * i + 1];
+    for (int s = tid; s < sp.parts; s += kTreeMergeThreads) {
+      const float2 mz = *reinterpret_cast<const float2*>(p.part_mz + 2 * (i0 + s * step));
+      const float top = fmaxf(M, mz.x);
+      Z = Z * tree_scale(M, top) + mz.y * tree_scale(mz.x, top);
+      M = top;
+      weight[s] = mz.x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, M, o), z = __shfl_xor_sync(0xffffffffu, Z, o);
       const float top = fmaxf(M, m);
       Z = Z * tree_scale(M, top) + z * tree_scale(m, top);
       M = top;
     }
-    const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    for (int d = threadIdx.x; d < p.t.d_c; d += kTreeMergeThreads) {
-      float acc = 0.f;
-      for (int s = 0; s < sp.parts; ++s) {
-        const int64_t i = (int64_t)(sp.base + s * sp.rb + rb) * p.rows_per_block + col;
-        acc += tree_scale(p.part_mz[2 * i], M) * p.part_o[i * p.t.d_c + d];
-      }
-      out[d] = from_f32<T>(acc * inv);
+    if (lane == 0) warp_mz[warp] = make_float2(M, Z);
+    __syncthreads();
+    M = -INFINITY;
+    Z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTreeMergeThreads / 32; ++w) {
+      const float2 mz = warp_mz[w];
+      const float top = fmaxf(M, mz.x);
+      Z = Z * tree_scale(M, top) + mz.y * tree_scale(mz.x, top);
+      M = top;
     }
-    if (lse && threadIdx.x == 0) *lse = Z == 0.f ? -INFINITY : kTreeLn2 * (M + log2f(Z));
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+    for (int s = tid; s < sp.parts; s += kTreeMergeThreads) weight[s] = tree_scale(weight[s], M) * inv;
+    __syncthreads();
+    for (int q = tid; q < quads; q += kTreeMergeThreads) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* o = p.part_o + i0 * p.t.d_c + 4 * q;
+      constexpr int kAtOnce = 8;
+      for (int s0 = 0; s0 < sp.parts; s0 += kAtOnce) {
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          if (s0 + u < sp.parts) v[u] = *reinterpret_cast<const float4*>(o + (s0 + u) * step * p.t.d_c);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          if (s0 + u < sp.parts) {
+            const float w = weight[s0 + u];
+            acc.x = fmaf(w, v[u].x, acc.x); acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z); acc.w = fmaf(w, v[u].w, acc.w);
+          }
+      }
+      store4(out + 4 * q, acc);
+    }
+    if (lse && tid == 0) *lse = Z == 0.f ? -INFINITY : kTreeLn2 * (M + log2f(Z));
+    __syncthreads();             // `weight` is free again
   }
 }
 
