@@ -73,6 +73,31 @@ LCA_HD int tree_least(const Lanes& w, const Seq& seq, int B, int most, int64_t l
   return lo;
 }
 
+// The same for up to count() sequences, lane b with sequence b's work: every lane tries a length of its own, so
+// a few rounds do.
+template <class Lanes>
+LCA_HD int tree_least_few(const Lanes& w, const TreeWork& own, int B, int most, int64_t limit) {
+  int lo = 1, hi = most + 1;                   // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + w.count() - 1) / w.count();
+    const int S = lo + w.lane() * step < hi ? lo + w.lane() * step : hi;     // hi: known to do (or none does)
+    int64_t units = 0;
+    for (int b = 0; b < B; ++b) {
+      const int rb = w.get(own.rb, b), tiles = w.get(own.tiles, b);
+      units += (int64_t)rb * (S <= most ? (tiles + S - 1) / S : 1);
+    }
+    const int at = w.first(S >= hi || units <= limit);
+    if (at < 0) {                              // none tried does: it lies above the last one
+      lo = lo + (w.count() - 1) * step + 1;
+    } else {
+      const int found = lo + at * step < hi ? lo + at * step : hi;
+      lo = at == 0 ? found : lo + (at - 1) * step + 1;
+      hi = found;
+    }
+  }
+  return lo;
+}
+
 // The cost of k waves with their least S (INT64_MAX: not possible).
 LCA_HD int64_t tree_cost(int k, int S, int most) {
   return S > most ? INT64_MAX : (int64_t)k * (S + kTreeUnitCost);

@@ -206,8 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  // ---- the cut: one warp per number of waves
+  // ---- the cut: one warp per number of waves.  Up to 32 sequences a lane keeps its own one's work.
+  const bool few = t.B <= 32;
+  TreeWork own = {0, 0};
+  if (few && lane < t.B) {
+    const TreeLens l = tree_lens(t, lane);
+    own = tree_work(l.n, l.d, t.H, N);
+  }
   auto seq = [&](int b) {
+    if (few) return own;                       // asked for b = lane only
     const TreeLens l = tree_lens(t, b);
     return tree_work(l.n, l.d, t.H, N);
   };
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
   for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (warp >= 2 && warp < 2 + kTreeMaxWaves) {
     const int k = warp - 1;
-    const int S = tree_least(lanes, seq, t.B, most, (int64_t)k * p.G);
+    const int S = few ? tree_least_few(lanes, own, t.B, most, (int64_t)k * p.G) : tree_least(lanes, seq, t.B, most, (int64_t)k * p.G);
     if (lane == 0) s_least[k - 1] = S;
   }
   ptx::tc_fence_before();
@@ -622,33 +629,48 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
       }
       if (sid == 0) *broken = 0ull;
       if (!meeting()) break;
-      if (sid < N) row_mz[sid].y = (red[sid] + red[N + sid]) + (red[2 * N + sid] + red[3 * N + sid]);
-      if (!meeting()) break;
       const bool whole = un.parts == 1;
       const int64_t row0 = (int64_t)un.b * t.T * t.H + (int64_t)un.rb * N;
-      if (whole ? p.lse && sid < rows : sid < rows && LCA_CHECK(t.err, u < p.slots, 0xD40)) {
-        const float2 mz = row_mz[sid];
-        if (whole) {
-          p.lse[row0 + sid] = mz.y == 0.f ? -INFINITY : kTreeLn2 * (mz.x + log2f(mz.y));
-        } else {
-          p.part_mz[2 * (u * N + sid)] = mz.x;
-          p.part_mz[2 * (u * N + sid) + 1] = mz.y;
+      if (sid < N) {
+        const float z = (red[sid] + red[N + sid]) + (red[2 * N + sid] + red[3 * N + sid]), m = row_mz[sid].x;
+        row_mz[sid].y = z == 0.f ? 0.f : 1.f / z;
+        if (sid < rows) {
+          if (!whole) {
+            if (LCA_CHECK(t.err, u < p.slots, 0xD40)) *reinterpret_cast<float2*>(p.part_mz + 2 * (u * N + sid)) = make_float2(m, z);
+          } else if (p.lse) {
+            p.lse[row0 + sid] = z == 0.f ? -INFINITY : kTreeLn2 * (m + log2f(z));
+          }
         }
       }
-      for (int m = 0; m < 4; ++m) {
-        float o[C];
-        tmem_load<C>(lane_base + kColO + N * m, o);
-        ptx::tmem_wait_ld();
-        const int dim = 128 * m + tok;
+      if (!meeting()) break;
+      // O^T: a thread has one dim and C rows of each block of 128 dims
+      const int mine = min(C, rows - C * half);                // rows of this thread
+      if (whole) {
+        __nv_bfloat16* dst = p.out + (row0 + C * half) * kDC + tok;
+        const float2* mz = row_mz + C * half;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int r = C * half + c;
-          if (r >= rows) break;
-          if (whole) {
-            const float z = row_mz[r].y;
-            p.out[(row0 + r) * kDC + dim] = __float2bfloat16_rn(z == 0.f ? 0.f : o[c] * (1.f / z));
-          } else if (LCA_CHECK(t.err, u < p.slots, 0xD41)) {
-            p.part_o[(u * N + r) * kDC + dim] = o[c];
+        for (int m = 0; m < 4; ++m) {
+          float o[C];
+          tmem_load<C>(lane_base + kColO + N * m, o);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if (c < mine) dst[c * kDC + 128 * m] = __float2bfloat16_rn(o[c] * mz[c].y);
+        }
+      } else if (LCA_CHECK(t.err, u < p.slots, 0xD41)) {
+        float* dst = p.part_o + (u * N + C * half) * kDC + tok;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float o[C];
+          tmem_load<C>(lane_base + kColO + N * m, o);
+          ptx::tmem_wait_ld();
+          if (mine == C) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) dst[c * kDC + 128 * m] = o[c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+              if (c < mine) dst[c * kDC + 128 * m] = o[c];
           }
         }
       }

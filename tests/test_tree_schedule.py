@@ -27,6 +27,28 @@ struct One {
   int get(int v, int) const { return v; }
   int64_t get(int64_t v, int) const { return v; }
 };
+// tree_least_few's search, its 32 lanes one after another
+static int least_few(const std::vector<TreeWork>& ws, int most, int64_t limit) {
+  int lo = 1, hi = most + 1;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    int at = -1;
+    for (int l = 0; l < 32 && at < 0; ++l) {
+      const int S = lo + l * step < hi ? lo + l * step : hi;
+      int64_t units = 0;
+      for (const auto& w : ws) units += (int64_t)w.rb * (S <= most ? (w.tiles + S - 1) / S : 1);
+      if (S >= hi || units <= limit) at = l;
+    }
+    if (at < 0) {
+      lo += 31 * step + 1;
+    } else {
+      const int found = lo + at * step < hi ? lo + at * step : hi;
+      lo = at == 0 ? found : lo + (at - 1) * step + 1;
+      hi = found;
+    }
+  }
+  return lo;
+}
 int main() {
   std::mt19937 rng(7);
   auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
@@ -49,6 +71,8 @@ int main() {
       if (s > 1 && s <= most && tree_units(one, seq, B, s - 1) <= (int64_t)k * G) return printf("not the least\n"), 1;
       const int64_t c = tree_cost(k, s, most);
       if (c < best) best = c, S = s;
+      if (B <= 32 && least_few(ws, most, (int64_t)k * G) != s) return printf("the searches differ\n"), 1;
+      if (B == 1 && tree_least_few(one, ws[0], B, most, (int64_t)k * G) != s) return printf("the searches differ\n"), 1;
     }
     std::vector<std::vector<int>> seen(B);
     for (int b = 0; b < B; ++b) seen[b].assign((size_t)ws[b].rb * ws[b].tiles, 0);
