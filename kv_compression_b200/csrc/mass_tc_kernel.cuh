@@ -33,8 +33,8 @@ namespace mtc {
 
 using ttc::kChunk;
 using ttc::Wait;
-constexpr int kThreads = ttc::kThreads;
-constexpr int kAddWarps = ttc::kSoftmaxWarps;
+constexpr int kAddWarps = 8;
+constexpr int kThreads = 32 * (2 + kAddWarps);
 constexpr int kBarAdd = 1;
 constexpr int kMaxSlots = 12;
 

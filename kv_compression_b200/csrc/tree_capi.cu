@@ -194,7 +194,7 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
   if (!allow_smem<ttc::lca_tree_tc_kernel<N>>(p->device, ttc::Layout<N>::kAlloc)) return LCA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tp.G, 1, 1);
-  cfg.blockDim = dim3(ttc::kThreads, 1, 1);
+  cfg.blockDim = dim3(ttc::Layout<N>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = ttc::Layout<N>::kAlloc;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

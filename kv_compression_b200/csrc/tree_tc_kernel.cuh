@@ -37,8 +37,8 @@
 // with an infinity or NaN is zeroed too and makes the sums of the rows that see
 // it NaN.
 //
-// Roles (320 threads): warp 0 loads, warp 1 issues the MMAs, warps 2-9 the
-// softmax (two per TMEM lane quarter, each with half of the rows).  Every wait
+// Roles: warp 0 loads, warp 1 issues the MMAs, the other 8 (N = 64: 16) do the
+// softmax: a warp has 32 tokens (a TMEM lane quarter) and 8 or 16 of the rows.  Every wait
 // is bounded: when one runs out the CTA records it, lets its copies and MMAs
 // land, frees TMEM and exits.
 #pragma once
@@ -55,8 +55,6 @@ namespace ttc {
 constexpr int kDC = 512, kDR = 64;
 constexpr int kChunk = 128 * 128;           // [128 tokens][64 bf16], 128-byte swizzle
 constexpr int kSlot = 2 * kChunk;           // 128 latent dims of a tile
-constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (2 + kSoftmaxWarps);
 constexpr int kMaxSlots = 5;
 constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
 constexpr float kRaise = 8.f;
@@ -67,14 +65,16 @@ constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 template <int N>
 struct Layout {
   static constexpr bool kAlias = N == 64;              // P in K's place
+  static constexpr int kSoftmaxWarps = N == 64 ? 16 : 8;
+  static constexpr int kThreads = 32 * (2 + kSoftmaxWarps);
   static constexpr int kSlots = N == 64 ? 4 : 5;
   static constexpr int kQChunk = N * 128;
   static constexpr int kOffK = kSlots * kSlot;
   static constexpr int kOffQ = kOffK + kChunk;
   static constexpr int kOffP = kAlias ? kOffK : kOffQ + 9 * kQChunk;
   static constexpr int kOffWord = kOffQ + 9 * kQChunk + (kAlias ? 0 : 128 * N * 2);   // mask words of the rows
-  static constexpr int kOffRed = kOffWord + 8 * N;     // float [4][N]
-  static constexpr int kOffM = kOffRed + 16 * N;       // float2 [N]: the rows' (M, Z)
+  static constexpr int kOffRed = kOffWord + 8 * N;     // float [2][4][N], used in turn
+  static constexpr int kOffM = kOffRed + 32 * N;       // float2 [N]: the rows' (M, Z)
   static constexpr int kOffBar = kOffM + 8 * N;
   static constexpr int kBars = 2 * kMaxSlots + 8;
   static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S of k waves; nodes with a broken row;
@@ -145,6 +145,28 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[C]) {
   else if constexpr (C == 16) ptx::tmem_ld16(addr, v);
   else ptx::tmem_ld8(addr, v);
 }
+// Reduces C values of each lane over the warp's 32 lanes, halving what is held with every exchange (C - 1
+// exchanges instead of 5 C): the return value is column lane / (32 / C)'s result.
+template <int C, class Op>
+__device__ __forceinline__ float fold(const float (&v)[C], int lane, Op op) {
+  float h[C / 2];
+  const bool up = lane & 16;
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i)
+    h[i] = op(up ? v[i + C / 2] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + C / 2], 16));
+  int off = 8;
+#pragma unroll
+  for (int n = C / 4; n > 0; n /= 2, off /= 2) {
+    const bool u = lane & off;
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i)
+      if (i < n) h[i] = op(u ? h[i + n] : h[i], __shfl_xor_sync(0xffffffffu, u ? h[i] : h[i + n], off));
+  }
+#pragma unroll
+  for (; off > 0; off /= 2) h[0] = op(h[0], __shfl_xor_sync(0xffffffffu, h[0], off));
+  return h[0];
+}
+
 // True if one of the 8 bf16 in `u` is an infinity or NaN.
 __device__ __forceinline__ bool any_nonfinite(uint4 u) {
   auto bad = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
@@ -152,11 +174,12 @@ __device__ __forceinline__ bool any_nonfinite(uint4 u) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(const __grid_constant__ Params p) {
   using L = Layout<N>;
   constexpr int kSlots = L::kSlots;
   constexpr int kKAt = L::kAlias ? 4 : 1;   // K is taken before this column slot of the tile (last where P waits for it)
-  constexpr int C = N / 2;                  // rows of a softmax thread
+  constexpr int kSoftmaxWarps = L::kSoftmaxWarps;
+  constexpr int C = 4 * N / kSoftmaxWarps;  // rows of a softmax thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -209,10 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
   // ---- the cut: one warp per number of waves.  Up to 32 sequences a lane keeps its own one's work.
   const bool few = t.B <= 32;
   TreeWork own = {0, 0};
+  TreeLens own_len = {0, 0, false};
   if (few && lane < t.B) {
-    const TreeLens l = tree_lens(t, lane);
-    own = tree_work(l.n, l.d, t.H, N);
+    own_len = tree_lens(t, lane);
+    own = tree_work(own_len.n, own_len.d, t.H, N);
   }
+  auto lens_of = [&](int b) {                  // for a whole warp
+    if (!few) return tree_lens(t, b);
+    return TreeLens{__shfl_sync(0xffffffffu, own_len.n, b), __shfl_sync(0xffffffffu, own_len.d, b), false};
+  };
   auto seq = [&](int b) {
     if (few) return own;                       // asked for b = lane only
     const TreeLens l = tree_lens(t, b);
@@ -251,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
-      const TreeLens l = tree_lens(t, un.b);
+      const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;
       // a tile's two halves of 64 rows; a second half without tokens is loaded from the first half's rows, and
       // zeroed later
@@ -446,14 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
   } else {
     // ---------------------------------------------------------------- softmax
     const int sw = warp - 2;
-    const int quarter = warp & 3, half = sw >> 2;     // TMEM lanes 32 quarter .., rows C half ..
+    const int quarter = warp & 3, part = sw >> 2;     // TMEM lanes 32 quarter .., rows C part ..
     const int tok = 32 * quarter + lane;              // this thread's token of a tile
     const int sid = tid - 64;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + C * half;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + C * part;
     unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord);
-    float* red = reinterpret_cast<float*>(smem + L::kOffRed);
+    float* reds = reinterpret_cast<float*>(smem + L::kOffRed);
+    int red_turn = 0;
     float2* row_mz = reinterpret_cast<float2*>(smem + L::kOffM);
-    uint8_t* pt = smem + L::kOffP + (C / 8) * half * 2048 + tok * 16;
+    uint8_t* pt = smem + L::kOffP + (C / 8) * part * 2048 + tok * 16;
     int64_t np = 0;
     int ev = 0, met = 0;        // events seen; meetings of the softmax warps
     bool ok = true;
@@ -465,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
       return ok;
     };
     // the sequences' records for the merge, by the first CTA
-    if (blockIdx.x == 0 && sw == 7) {
+    if (blockIdx.x == 0 && sw == kSoftmaxWarps - 1) {
       int64_t base = 0;
       for (int b0 = 0; b0 < t.B; b0 += 32) {
         const int b = b0 + lane;
@@ -485,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
     for (int64_t u = blockIdx.x; ok; u += p.G) {
       const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
       if (un.b < 0) break;
-      const TreeLens l = tree_lens(t, un.b);
+      const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;
       const int rows = min(N, l.d * t.H - un.rb * N);
       if (!meeting()) break;                           // the last unit's words and sums are read
@@ -549,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             const bool bk = in && ((*broken >> node) & 1ull);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-              const bool sees = in && ((words[C * half + c] >> node) & 1ull);
+              const bool sees = in && ((words[C * part + c] >> node) & 1ull);
               if (sees && bk) hurt |= 1u << c;
               if (!sees || bk) x[c] = -INFINITY;
             }
@@ -557,20 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
         }
         if (raise) {
           // M becomes the largest logit so far, row by row
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            float m = x[c];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) red[quarter * N + C * half + c] = m * kTreeLog2e;
-          }
+          float* red = reds + 4 * N * (red_turn++ & 1);
+          const float m0 = fold<C>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+          if (lane % (32 / C) == 0) red[quarter * N + C * part + lane / (32 / C)] = m0 * kTreeLog2e;
           if (!meeting()) break;
 #pragma unroll
           for (int c0 = 0; c0 < C; c0 += 8) {
             float f[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const int r = C * half + c0 + c;
+              const int r = C * part + c0 + c;
               const float m = fmaxf(fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])), -nM[c0 + c]);
               f[c] = ex2(-nM[c0 + c] - m);
               Z[c0 + c] *= f[c];
@@ -589,7 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             }
           }
           ptx::tmem_wait_st();
-          if (!meeting()) break;                               // `red` is free again
         }
         float top = -INFINITY;
 #pragma unroll
@@ -619,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
       if (!ok) break;
       ++ev;
       // ---- the unit's sums
+      float* red = reds + 4 * N * (red_turn++ & 1);
+      const float z0 = fold<C>(Z, lane, [](float a, float b) { return a + b; });
+      if (lane % (32 / C) == 0) red[quarter * N + C * part + lane / (32 / C)] = z0;
+      if (quarter == 0) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float z = Z[c];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (lane == 0) red[quarter * N + C * half + c] = z;
-        if (lane == 0 && quarter == 0) row_mz[C * half + c].x = -nM[c];
+        for (int c = 0; c < C; ++c)
+          if (lane == c) row_mz[C * part + c].x = -nM[c];
       }
       if (sid == 0) *broken = 0ull;
       if (!meeting()) break;
@@ -644,10 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
       }
       if (!meeting()) break;
       // O^T: a thread has one dim and C rows of each block of 128 dims
-      const int mine = min(C, rows - C * half);                // rows of this thread
+      const int mine = min(C, rows - C * part);                // rows of this thread
       if (whole) {
-        __nv_bfloat16* dst = p.out + (row0 + C * half) * kDC + tok;
-        const float2* mz = row_mz + C * half;
+        __nv_bfloat16* dst = p.out + (row0 + C * part) * kDC + tok;
+        const float2* mz = row_mz + C * part;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           float o[C];
@@ -658,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_tree_tc_kernel(const __grid_c
             if (c < mine) dst[c * kDC + 128 * m] = __float2bfloat16_rn(o[c] * mz[c].y);
         }
       } else if (LCA_CHECK(t.err, u < p.slots, 0xD41)) {
-        float* dst = p.part_o + (u * N + C * half) * kDC + tok;
+        float* dst = p.part_o + (u * N + C * part) * kDC + tok;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           float o[C];
