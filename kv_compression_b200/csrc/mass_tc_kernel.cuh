@@ -47,7 +47,8 @@ struct Layout {
   static constexpr int kOffRing = 9 * kStay;
   static constexpr int kOffOff = kOffRing + kSlots * kChunk;               // float [2][N] offsets of the rows
   static constexpr int kOffPart = kOffOff + 8 * N;                         // float [128]
-  static constexpr int kOffBar = kOffPart + 512;
+  static constexpr int kOffGap = kOffPart + 512;                           // u32 [2][4] rows that add nothing
+  static constexpr int kOffBar = kOffGap + 32;
   static constexpr int kBars = 2 * kMaxSlots + 7;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kBytes = kOffMisc + 16;
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + C * half;
     float* off = reinterpret_cast<float*>(smem + L::kOffOff);
     float* part = reinterpret_cast<float*>(smem + L::kOffPart);
+    uint32_t* gap = reinterpret_cast<uint32_t*>(smem + L::kOffGap);
     if (blockIdx.x == 0 && sw == 7) {
       int64_t base = 0;
       for (int b0 = 0; b0 < t.B; b0 += 32) {
@@ -327,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       const int pos0 = s.tile * kTreeTile;
       const bool special = pos0 + kTreeTile > l.n;     // drafted tokens, or the end, in this tile
       if (sid < N) off[buf * N + sid] = o_next;
-      const bool none = sid < N && o_next == INFINITY;
+      const uint32_t empty_rows = __ballot_sync(0xffffffffu, o_next == INFINITY);
+      if (sid < N && lane == 0) gap[4 * buf + sw] = empty_rows;
       const Step at = s;
       const TreeLens lat = l;
       next(s);
@@ -343,37 +346,45 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       }
       fresh = false;
       const bool live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45);
-      const bool gaps = ptx::named_bar_or(kBarAdd, 32 * kAddWarps, none || !live);
-      if (gaps && ptx::named_bar_or(kBarAdd, 32 * kAddWarps, !live)) break;
+      if (ptx::named_bar_or(kBarAdd, 32 * kAddWarps, !live)) break;
       ptx::tc_fence_after();
       float a0 = 0.f, a1 = 0.f;
-      int node_of = (at.rb * N + C * half) / t.H, in_node = (at.rb * N + C * half) - node_of * t.H;
+      constexpr int W = C < 32 ? C : 32;
 #pragma unroll
-      for (int c0 = 0; c0 < C; c0 += (C < 32 ? C : 32)) {
-        constexpr int W = C < 32 ? C : 32;
+      for (int c0 = 0; c0 < C; c0 += W) {
         float x[W];
         ttc::tmem_load<W>(addr + N * buf + c0, x);
         ptx::tmem_wait_ld();
-        const float* o = off + buf * N + C * half + c0;
-        if (!gaps && !special) {
-#pragma unroll
-          for (int c = 0; c < W; c += 4) {
-            const float4 o4 = *reinterpret_cast<const float4*>(o + c);
-            a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o4.x));
-            a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o4.y));
-            a0 += ttc::ex2(fmaf(x[c + 2], kTreeLog2e, -o4.z));
-            a1 += ttc::ex2(fmaf(x[c + 3], kTreeLog2e, -o4.w));
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            const float oc = o[c];
-            if (oc != INFINITY && ((vis >> node_of) & 1ull)) a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -oc));
-            if (++in_node == t.H) {
-              in_node = 0;
-              ++node_of;
+        const int col0 = C * half + c0;
+        const float* o = off + buf * N + col0;
+        const uint32_t all = W == 32 ? ~0u : (1u << (W & 31)) - 1u;
+        const uint32_t gaps = (gap[4 * buf + col0 / 32] >> (col0 % 32)) & all;
+        if (special || gaps != 0u) {
+          // the rows of these that see this thread's token, and are there; the others' logits become -inf
+          uint32_t sees = ~gaps;
+          if (special) {
+            int node = (at.rb * N + col0) / t.H, left = t.H - (at.rb * N + col0 - node * t.H);
+            for (int c = 0; c < W; ++node, left = t.H) {
+              const int n = min(left, W - c);
+              if (!((vis >> node) & 1ull)) sees &= ~((n == 32 ? ~0u : (1u << n) - 1u) << c);
+              c += n;
             }
           }
+#pragma unroll
+          for (int c = 0; c < W; ++c) x[c] = (sees >> c) & 1u ? x[c] : -INFINITY;
+          if (gaps != 0u) {                            // -inf - inf: an offset that stands for nothing is passed over
+#pragma unroll
+            for (int c = 0; c < W; ++c) a0 += (sees >> c) & 1u ? ttc::ex2(fmaf(x[c], kTreeLog2e, -o[c])) : 0.f;
+            continue;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < W; c += 4) {
+          const float4 o4 = *reinterpret_cast<const float4*>(o + c);
+          a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o4.x));
+          a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o4.y));
+          a0 += ttc::ex2(fmaf(x[c + 2], kTreeLog2e, -o4.z));
+          a1 += ttc::ex2(fmaf(x[c + 3], kTreeLog2e, -o4.w));
         }
       }
       ptx::tc_fence_before();
