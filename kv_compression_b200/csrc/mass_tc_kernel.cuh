@@ -123,14 +123,21 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
   }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  auto seq = [&](int b) {
-    const TreeLens l = tree_lens(t, b);
+  // up to 32 sequences a lane keeps its own one's lengths
+  const bool few = t.B <= 32;
+  auto work = [&](const TreeLens& l) {
     TreeWork w = tree_work(l.n, l.d, t.H, N);
     if (l.d == 0 && l.n > 0) {        // nothing to add, but the old sums are scaled all the same
       w.rb = 1;
       w.tiles = (l.n + kTreeTile - 1) / kTreeTile;
     }
     return w;
+  };
+  const TreeLens own = few && lane < t.B ? tree_lens(t, lane) : TreeLens{0, 0, false};
+  const TreeWork own_work = work(own);
+  auto seq = [&](int b) { return few ? own_work : work(tree_lens(t, b)); };     // few: asked for b = lane only
+  auto lens_of = [&](int b) {         // for a whole warp
+    return few ? TreeLens{lanes.get(own.n, b), lanes.get(own.d, b), false} : tree_lens(t, b);
   };
   const int64_t U = tree_units(lanes, seq, t.B, 1);
   // CTA c of the G used (no more than there are steps): steps [c U / G, (c + 1) U / G)
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
   Step st0 = {0, 0, 0, 1, 1};
   if (u0 < u1) {
     const TreeUnit x = tree_unit(lanes, seq, t.B, 1, u0);
-    const TreeWork w = seq(x.b);
+    const TreeWork w = work(lens_of(x.b));
     st0 = Step{x.b, x.t0, x.rb, w.tiles, w.rb};
   }
   auto next = [&](Step& s) {
@@ -149,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     s.tile = 0;
     s.tiles = 0;
     while (s.tiles == 0 && ++s.b < t.B) {
-      const TreeWork w = seq(s.b);
+      const TreeWork w = work(lens_of(s.b));
       s.tiles = w.tiles;
       s.rbs = w.rb;
     }
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     int last_b = -1, last_tile = -1;
     int r0 = 0, r1 = 0;
     auto rows_of = [&](const Step& x, int& a, int& b) {
-      const TreeLens l = tree_lens(t, x.b);
+      const TreeLens l = lens_of(x.b);
       const int pos = x.tile * kTreeTile;
       a = (int)tree_row(t, x.b, pos, 0xB06);
       b = pos + 64 < l.n + l.d ? (int)tree_row(t, x.b, pos + 64, 0xB06) : a;
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     int segment = 0;
     bool from_start = s.rb == 0, fresh = true;
     float acc = 0.f;
-    TreeLens l = tree_lens(t, s.b);
+    TreeLens l = lens_of(s.b);
     // a row's offset; rows that add nothing have an infinite one.  Read a step ahead.
     auto offset = [&](const Step& at, int d) {
       const int r = at.rb * N + sid;
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       const TreeLens lat = l;
       next(s);
       if (u + 1 < u1) {
-        if (s.b != at.b) l = tree_lens(t, s.b);
+        if (s.b != at.b) l = lens_of(s.b);
         o_next = offset(s, l.d);
       }
       if (fresh && special) {
