@@ -117,12 +117,23 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _expect(what: str, t, dtype, *shape) -> None:
-    """`t` is a contiguous CUDA tensor of this type and shape (None: any size); LCA_ERR_INVALID_ARG otherwise."""
-    if (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape)
-            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise LcaError(LCA_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}; "
-                       f"wanted a contiguous CUDA tensor of {dtype} {tuple('*' if n is None else n for n in shape)}")
+def _refuse(what: str, t, dtype, shape) -> None:
+    raise LcaError(LCA_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}; "
+                   f"wanted a contiguous CUDA tensor of {dtype} {shape}")
+
+
+def _expect(what: str, t, dtype, shape) -> int:
+    """The address of `t`, a contiguous CUDA tensor of this type and shape; LCA_ERR_INVALID_ARG if it is none."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
+        _refuse(what, t, dtype, shape)
+    return t.data_ptr()
+
+
+def _expect_rows(what: str, t, dtype, rows: int) -> int:
+    """The same for a matrix of `rows` rows of any length."""
+    if not (t.dtype is dtype and t.dim() == 2 and t.shape[0] == rows and t.is_contiguous() and t.is_cuda):
+        _refuse(what, t, dtype, (rows, "*"))
+    return t.data_ptr()
 
 
 def _stream_handle(stream) -> int | None:
@@ -152,6 +163,10 @@ class Plan:
         _check(self._lib.lca_plan_create(self.B, self.H, self.d_c, self.d_r, dt, self.max_L,
                                          ctypes.byref(h)), "lca_plan_create")
         self._h = h
+        self._device = torch.cuda.current_device()
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._elem = torch.bfloat16 if self.dtype == "bf16" else torch.float32
+        self._f32, self._i32, self._i64 = torch.float32, torch.int32, torch.int64
 
     @property
     def handle(self) -> int:
@@ -259,35 +274,28 @@ class Plan:
 
     # ------------------------------------------------------------ drafted tokens and eviction
 
-    def _elem(self):
-        import torch
-        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+    def _call_stream(self, stream) -> int:
+        """The handle of `stream`, or of the current one of the plan's device."""
+        return self._raw_stream(self._device) if stream is None else stream.cuda_stream
 
     def _cache_args(self, c_pool, k_pool, page_size: int, block_table):
         """The cache arguments of the C calls, checked: pools [rows, d] (or [B, capacity, d]) and an int32
         block_table [B, max_pages], or None for a contiguous cache with page_size rows a sequence."""
-        import torch
         if c_pool.dim() == 3:
             c_pool, k_pool = c_pool.flatten(0, 1), k_pool.flatten(0, 1)
         rows = c_pool.shape[0]
-        _expect("c_pool", c_pool, self._elem(), rows, self.d_c)
-        _expect("k_pool", k_pool, self._elem(), rows, self.d_r)
-        if block_table is not None:
-            _expect("block_table", block_table, torch.int32, self.B, None)
-        return (_ptr(c_pool), _ptr(k_pool), rows // page_size if page_size > 0 else 0, page_size, _ptr(block_table),
-                1 if block_table is None else block_table.shape[1])
+        c, k = _expect("c_pool", c_pool, self._elem, (rows, self.d_c)), _expect("k_pool", k_pool, self._elem, (rows, self.d_r))
+        pages = rows // page_size if page_size > 0 else 0
+        if block_table is None:
+            return c, k, pages, page_size, None, 1
+        return c, k, pages, page_size, _expect_rows("block_table", block_table, self._i32, self.B), block_table.shape[1]
 
     def _draft_args(self, q_c, q_r, seq_lens, draft_lens, mask):
-        import torch
-        T = q_c.shape[1]
-        _expect("q_c", q_c, self._elem(), self.B, T, self.H, self.d_c)
-        _expect("q_r", q_r, self._elem(), self.B, T, self.H, self.d_r)
-        _expect("seq_lens", seq_lens, torch.int32, self.B)
-        if draft_lens is not None:
-            _expect("draft_lens", draft_lens, torch.int32, self.B)
-        if mask is not None:
-            _expect("mask", mask, torch.int64, self.B, T)
-        return T
+        B, T, i32 = self.B, q_c.shape[1], self._i32
+        return (T, _expect("q_c", q_c, self._elem, (B, T, self.H, self.d_c)),
+                _expect("q_r", q_r, self._elem, (B, T, self.H, self.d_r)), _expect("seq_lens", seq_lens, i32, (B,)),
+                None if draft_lens is None else _expect("draft_lens", draft_lens, i32, (B,)),
+                None if mask is None else _expect("mask", mask, self._i64, (B, T)))
 
     def tree_workspace(self, n_draft: int, stream=None):
         """A workspace for tree_decode and attn_mass with up to n_draft drafted tokens a sequence: keep one per
@@ -296,10 +304,17 @@ class Plan:
         size = int(self._lib.lca_tree_workspace(self._h, n_draft))
         if size < 0:
             raise LcaError(LCA_ERR_INVALID_ARG, f"tree_workspace: n_draft {n_draft} outside 1 .. {MAX_DRAFT}")
-        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        ws = torch.empty(size, dtype=torch.uint8, device=self._device)
         if stream is not None:
             ws.record_stream(stream)
         return ws
+
+    def _workspace(self, workspace, T: int, stream) -> tuple[int, int]:
+        if workspace is None:
+            workspace = self.tree_workspace(T, stream)
+        elif not (workspace.is_cuda and workspace.is_contiguous()):
+            _refuse("workspace", workspace, "any type", "(*,)")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def tree_decode(self, q_c, q_r, c_pool, k_pool, page_size: int, block_table, seq_lens, out, lse=None, mask=None,
                     draft_lens=None, workspace=None, stream=None) -> None:
@@ -307,63 +322,54 @@ class Plan:
         and block_table as for decode_paged, or block_table None and pools [B, page_size, d]; seq_lens, draft_lens
         int32 [B]; mask int64 [B,T] (see tree_mask), None for a chain; out [B,T,H,d_c] of the plan's type, lse
         [B,T,H] fp32 or None."""
-        import torch
-        T = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
+        T, qc, qr, lens, drafts, words = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        _expect("out", out, self._elem(), self.B, T, self.H, self.d_c)
-        if lse is not None:
-            _expect("lse", lse, torch.float32, self.B, T, self.H)
-        if workspace is None:
-            workspace = self.tree_workspace(T, stream)
-        _check(self._lib.lca_tree_decode(self._h, _ptr(q_c), _ptr(q_r), T, *cache, _ptr(seq_lens), _ptr(draft_lens),
-                                         _ptr(mask), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                         _stream_handle(stream)), "lca_tree_decode")
+        o = _expect("out", out, self._elem, (self.B, T, self.H, self.d_c))
+        z = None if lse is None else _expect("lse", lse, self._f32, (self.B, T, self.H))
+        ws, size = self._workspace(workspace, T, stream)
+        st = self._lib.lca_tree_decode(self._h, qc, qr, T, *cache, lens, drafts, words, o, z, ws, size,
+                                       self._call_stream(stream))
+        if st:
+            raise LcaError(st, "lca_tree_decode")
 
     def attn_mass(self, q_c, q_r, c_pool, k_pool, page_size: int, block_table, seq_lens, lse, scores, prev=None,
                   decay: float = 1.0, mask=None, draft_lens=None, workspace=None, stream=None) -> None:
         """lca_attn_mass: scores [B, stride] fp32 = decay * prev + the attention weight each token receives from
         these queries (lse from tree_decode; +inf leaves a row out).  prev may be scores, None stands for zeros."""
-        import torch
-        T = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
+        T, qc, qr, lens, drafts, words = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        _expect("lse", lse, torch.float32, self.B, T, self.H)
-        _expect("scores", scores, torch.float32, self.B, None)
-        if prev is not None:
-            _expect("prev", prev, torch.float32, self.B, scores.shape[1])
-        if workspace is None:
-            workspace = self.tree_workspace(T, stream)
-        _check(self._lib.lca_attn_mass(self._h, _ptr(q_c), _ptr(q_r), T, *cache, _ptr(seq_lens), _ptr(draft_lens),
-                                       _ptr(mask), _ptr(lse), _ptr(prev), float(decay), _ptr(scores),
-                                       scores.shape[1], _ptr(workspace), workspace.numel(), _stream_handle(stream)),
-               "lca_attn_mass")
+        z = _expect("lse", lse, self._f32, (self.B, T, self.H))
+        s = _expect_rows("scores", scores, self._f32, self.B)
+        before = None if prev is None else _expect("prev", prev, self._f32, scores.shape)
+        ws, size = self._workspace(workspace, T, stream)
+        st = self._lib.lca_attn_mass(self._h, qc, qr, T, *cache, lens, drafts, words, z, before, decay, s,
+                                     scores.shape[1], ws, size, self._call_stream(stream))
+        if st:
+            raise LcaError(st, "lca_attn_mass")
 
     def evict_select(self, scores, seq_lens, n_sink: int, n_recent: int, kept, kept_lens, stream=None) -> None:
         """lca_evict_select: the rows to keep, kept [B, budget] int32 rising, kept_lens [B] int32, from scores
         [B, stride] fp32: the first n_sink, the last n_recent and the largest sums between."""
-        import torch
-        _expect("scores", scores, torch.float32, self.B, None)
-        _expect("seq_lens", seq_lens, torch.int32, self.B)
-        _expect("kept", kept, torch.int32, self.B, None)
-        _expect("kept_lens", kept_lens, torch.int32, self.B)
-        _check(self._lib.lca_evict_select(self._h, _ptr(scores), scores.shape[1], _ptr(seq_lens), n_sink, n_recent,
-                                          kept.shape[1], _ptr(kept), _ptr(kept_lens), _stream_handle(stream)),
-               "lca_evict_select")
+        B, i32 = self.B, self._i32
+        st = self._lib.lca_evict_select(self._h, _expect_rows("scores", scores, self._f32, B), scores.shape[1],
+                                        _expect("seq_lens", seq_lens, i32, (B,)), n_sink, n_recent, kept.shape[-1],
+                                        _expect_rows("kept", kept, i32, B), _expect("kept_lens", kept_lens, i32, (B,)),
+                                        self._call_stream(stream))
+        if st:
+            raise LcaError(st, "lca_evict_select")
 
     def cache_compact(self, c_pool, k_pool, page_size: int, block_table, src, n_src, dst0=None, scores=None,
                       stream=None) -> None:
         """lca_cache_compact: row dst0[b] + j of sequence b becomes its row src[b, j], j < n_src[b], in place
         (with the sums, if given): an eviction's kept rows, or a committed path of drafted tokens."""
-        import torch
+        B, i32 = self.B, self._i32
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        _expect("src", src, torch.int32, self.B, None)
-        _expect("n_src", n_src, torch.int32, self.B)
-        if dst0 is not None:
-            _expect("dst0", dst0, torch.int32, self.B)
-        if scores is not None:
-            _expect("scores", scores, torch.float32, self.B, None)
-        _check(self._lib.lca_cache_compact(self._h, *cache, _ptr(src), src.shape[1], _ptr(n_src), _ptr(dst0),
-                                           _ptr(scores), 0 if scores is None else scores.shape[1],
-                                           _stream_handle(stream)), "lca_cache_compact")
+        to = None if dst0 is None else _expect("dst0", dst0, i32, (B,))
+        s, stride = (None, 0) if scores is None else (_expect_rows("scores", scores, self._f32, B), scores.shape[1])
+        st = self._lib.lca_cache_compact(self._h, *cache, _expect_rows("src", src, i32, B), src.shape[1],
+                                         _expect("n_src", n_src, i32, (B,)), to, s, stride, self._call_stream(stream))
+        if st:
+            raise LcaError(st, "lca_cache_compact")
 
     def device_error(self, stream=None) -> int:
         return int(self._lib.lca_get_device_error(self._h, _stream_handle(stream)))
