@@ -509,7 +509,7 @@ lca_status lca_attn_mass(lca_plan *plan, const void *q_c, const void *q_r, int n
  * largest sums, as make `budget`; equal sums (0 and -0 are) go to the lower row, NaN
  * counts as the smallest.  With n_b <= budget every row is kept.
  *   scores     device fp32 [B][score_stride]; rows from n_b on are not read
- *   seq_lens   device int32 [B]: 0 <= n_b <= min(max_L, score_stride)
+ *   seq_lens   device int32 [B]: 0 <= n_b <= min(max_L, score_stride, 2^30)
  *   kept       device int32 [B][budget]: the kept rows of each sequence, rising;
  *              entries from kept_lens[b] on are left as they were
  *   kept_lens  device int32 [B]: min(n_b, budget); 0 where n_b is out of range

@@ -17,13 +17,16 @@ namespace lca {
 // All rows stay where n <= budget.  The kept rows are written in rising order.
 //
 // The sums map to unsigned keys of the same order.  A sequence belongs to a
-// cluster of CTAs, each with a contiguous run of its rows, whose keys it reads
-// once and keeps in shared memory.  The key of the last row kept is found 11, 11
-// and 10 bits at a time: a histogram per CTA of the keys that share the bits
-// found so far, added up over the cluster by every CTA for itself.  Then each
-// warp counts the kept rows of its run, the counts before it (its CTA's, and
-// the lower CTAs' totals) say where its rows go, and it writes them in order.
-// What bounds it is latency: five cluster barriers and three histograms.
+// cluster of CTAs, each with a contiguous run of its rows and each thread with
+// E consecutive ones, whose keys are read once (128-byte lines) and kept in
+// shared memory, thread t's e-th at [e][t].  The key of the last row kept is found 8 bits at a
+// time: a histogram per CTA of the keys that share the bits found so far, added
+// up over the cluster by every CTA for itself; it ends early once all rows that
+// share the bits found are to stay.  A scan of the threads' counts (and the
+// lower CTAs' totals) then says where each thread's rows go.
+// What bounds it is latency: up to four histograms, each with a cluster barrier.
+// (11 bits at a time, three histograms, took 30 us instead of 20 at 8 x 131072
+// rows: adding 2048 bins over 8 CTAs costs more than a further round.)
 struct SelectParams {
   const float* scores;          // [B][stride]
   int64_t stride;
@@ -46,19 +49,18 @@ __device__ __forceinline__ uint32_t select_key(float x) {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectBins = 2048;
-constexpr int kSelectKeep = 40960;          // keys of a CTA in shared memory; later ones are read again
+constexpr int kSelectBins = 256;
+constexpr int kSelectKeep = 40;             // rows of a thread whose keys stay in shared memory; later ones are read again
+constexpr int kSelectStride = kSelectThreads + 1;   // of keys[e]: what one warp reads from memory falls into all banks
 constexpr int kSelectMaxCtas = 8;
 
-__host__ __device__ inline size_t select_smem(int64_t run) {
-  const int64_t keys = run < kSelectKeep ? run : kSelectKeep;
-  return sizeof(int) * (3 * kSelectBins + (size_t)keys);
-}
-
-// Rows a CTA of `ctas` takes of n: a multiple of 32 x warps, so that every warp's run starts on a 128-byte line.
-__host__ __device__ inline int64_t select_run(int64_t n, int ctas) {
+// Rows of a thread, of n over `ctas` CTAs.
+__host__ __device__ inline int select_each(int64_t n, int ctas) {
   const int64_t per = (n + ctas - 1) / ctas;
-  return (per + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+  return (int)((per + kSelectThreads - 1) / kSelectThreads);
+}
+__host__ __device__ inline size_t select_smem(int each) {
+  return sizeof(int) * (4 * kSelectBins + (size_t)(each < kSelectKeep ? each : kSelectKeep) * kSelectStride);
 }
 
 __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
@@ -66,13 +68,20 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::mapa(ptx::smem_u32(p), rank)) : "memory");
   return v;
 }
-
 __device__ __forceinline__ int4 ld_cluster4(const int* p, uint32_t rank) {
   int4 v;
   asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(ptx::mapa(ptx::smem_u32(p), rank))
                : "memory");
+  return v;
+}
+__device__ __forceinline__ int warp_scan(int v, int lane) {     // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
   return v;
 }
 // The sum of the warps' values below `warp`.
@@ -85,10 +94,10 @@ __device__ __forceinline__ int warp_prefix(const int* sums, int warp, int lane) 
 
 __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const SelectParams p) {
   extern __shared__ int select_dyn[];
-  int* hist = select_dyn;                                       // [3][2048]
-  uint32_t* keys = reinterpret_cast<uint32_t*>(select_dyn + 3 * kSelectBins);
+  int* hist = select_dyn;                                       // [4][256]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(select_dyn + 4 * kSelectBins);
   __shared__ int warp_sum[kSelectWarps], warp_eq[kSelectWarps];
-  __shared__ int s_bin, s_above;
+  __shared__ int s_bin, s_above, s_count;
   __shared__ int totals[2];                                     // rows kept for sure, rows of the last key
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = p.ctas, rank = blockIdx.x % ctas, b = blockIdx.x / ctas;
@@ -107,148 +116,126 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
     return;
   }
   const float* x = p.scores + (int64_t)b * p.stride;
-  const int run = (int)select_run(n, ctas);                     // this CTA: rows [r0, r1)
-  const int r0 = (int)min((int64_t)n, (int64_t)rank * run), r1 = min(n, r0 + run);
+  const int each = select_each(n, ctas), run = each * kSelectThreads;
+  const int r0 = (int)min((int64_t)n, (int64_t)rank * run), r1 = (int)min((int64_t)n, (int64_t)r0 + run);   // this CTA's rows
   const int lo = p.n_sink, hi = n - p.n_recent;                 // rows that compete
-  auto key_of = [&](int i) { return i - r0 < kSelectKeep ? keys[i - r0] : select_key(x[i]); };
-  for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) hist[i] = 0;
+  const int first = r0 + tid * each;                            // this thread's rows
+  const int mine = max(0, min(each, r1 - first));
+  auto key_of = [&](int e) { return e < kSelectKeep ? keys[e * kSelectStride + tid] : select_key(x[first + e]); };
+  hist[tid] = 0;
   __syncthreads();
   int need = p.budget - p.n_sink - p.n_recent;                  // rows to take of [lo, hi)
   const bool any = need > 0;
   uint32_t prefix = 0, have = 0;                                // bits of the last key found; their mask
-  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    int* h = hist + pass * kSelectBins;
+  {
+    // the run's keys, line by line; row j of it is thread j / each's e = j % each
+    const uint32_t magic = (uint32_t)(((1ull << 32) + each - 1) / each);   // j / each = j magic >> 32 for these j
     constexpr int kUnroll = 16;
-    for (int i0 = r0; i0 < r1; i0 += kUnroll * kSelectThreads) {
-      uint32_t k[kUnroll];
+    for (int u0 = 0; u0 < each; u0 += kUnroll) {
+      float v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kSelectThreads + tid;
-        k[u] = 0;
-        if (i < r1) k[u] = pass == 0 ? select_key(x[i]) : key_of(i);
+        const int i = r0 + (u0 + u) * kSelectThreads + tid;
+        v[u] = u0 + u < each && i < r1 ? x[i] : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kSelectThreads + tid;
-        if (i >= r1) continue;
-        if (pass == 0 && i - r0 < kSelectKeep) keys[i - r0] = k[u];
-        if (i >= lo && i < hi && (k[u] & have) == prefix) atomicAdd(&h[(k[u] >> kShift[pass]) & ((1u << kBits[pass]) - 1u)], 1);
+        const int j = (u0 + u) * kSelectThreads + tid, i = r0 + j;
+        if (u0 + u >= each || i >= r1) continue;
+        const uint32_t k = select_key(v[u]);
+        const int c = each == 1 ? j : (int)__umulhi((uint32_t)j, magic), e = j - c * each;
+        if (e < kSelectKeep) keys[e * kSelectStride + c] = k;
+        if (i >= lo && i < hi) atomicAdd(&hist[k >> 24], 1);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int pass = 0; any; ++pass) {
+    int* h = hist + pass * kSelectBins;
+    const int shift = 24 - 8 * pass;
+    if (pass > 0) {
+      for (int e = 0; e < mine; ++e) {
+        const uint32_t k = key_of(e);
+        const int i = first + e;
+        if ((k & have) == prefix && i >= lo && i < hi) atomicAdd(&h[(k >> shift) & 255u], 1);
       }
     }
     ptx::cluster_sync();                                        // (also the CTA's own barrier)
-    if (any) {
-      // thread t < 512 has the four bins from 2047 - 4t down; their counts over the cluster, scanned from the top
-      int4 c = make_int4(0, 0, 0, 0);                           // .w the highest bin
+    if (warp < 2) {
+      // thread t < 64 has the four bins from 255 - 4t down; their counts over the cluster, scanned from the top
       const int bin0 = kSelectBins - 4 - 4 * tid;
-      if (tid < kSelectBins / 4) {
-        int4 v[kSelectMaxCtas];
+      int4 v[kSelectMaxCtas], c = make_int4(0, 0, 0, 0);        // .w the highest bin
 #pragma unroll
-        for (int r = 0; r < kSelectMaxCtas; ++r) v[r] = r < ctas ? ld_cluster4(h + bin0, r) : make_int4(0, 0, 0, 0);
+      for (int r = 0; r < kSelectMaxCtas; ++r) v[r] = r < ctas ? ld_cluster4(h + bin0, r) : make_int4(0, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < kSelectMaxCtas; ++r) {
-          c.x += v[r].x; c.y += v[r].y; c.z += v[r].z; c.w += v[r].w;
-        }
+      for (int r = 0; r < kSelectMaxCtas; ++r) {
+        c.x += v[r].x; c.y += v[r].y; c.z += v[r].z; c.w += v[r].w;
       }
-      int incl = c.x + c.y + c.z + c.w;
-      const int mine = incl;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int above = warp_prefix(warp_sum, warp, lane) + incl - mine;      // rows in higher bins
+      const int sum = c.x + c.y + c.z + c.w, incl = warp_scan(sum, lane);
+      if (warp == 0 && lane == 31) warp_sum[0] = incl;
+      ptx::named_bar_sync(1, 64);
+      int above = incl - sum + (warp == 1 ? warp_sum[0] : 0);   // rows in higher bins
       const int count[4] = {c.w, c.z, c.y, c.x};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (above < need && need <= above + count[q]) {
           s_bin = bin0 + 3 - q;
           s_above = above;
+          s_count = count[q];
         }
         above += count[q];
       }
-      __syncthreads();
-      prefix |= (uint32_t)s_bin << kShift[pass];
-      have |= ((1u << kBits[pass]) - 1u) << kShift[pass];
-      need -= s_above;
     }
+    __syncthreads();
+    prefix |= (uint32_t)s_bin << shift;
+    have |= 255u << shift;
+    need -= s_above;
+    if (s_count == need || pass == 3) break;
   }
-  // a warp's rows: kept for sure (by place, or by a larger key), or of the last key
-  const int per_warp = run / kSelectWarps;
-  const int w0 = min(r1, r0 + warp * per_warp), w1 = min(r1, w0 + per_warp);
-  auto judge = [&](int i, bool& sure, bool& eq) {
-    sure = eq = false;
-    if (i >= w1) return;
-    if (i < lo || i >= hi) {
-      sure = true;
-    } else if (any) {
-      const uint32_t k = key_of(i);
-      sure = k > prefix;
-      eq = k == prefix;
-    }
+  // a thread's rows: kept for sure (by place, or by a larger key), or of the last key
+  auto judge = [&](int e, bool& sure, bool& eq) {
+    const int i = first + e;
+    const bool place = i < lo || i >= hi;
+    const uint32_t k = any && !place ? key_of(e) & have : 0u;
+    sure = place || (any && k > prefix);
+    eq = !place && any && k == prefix;
   };
-  // lane j keeps the votes on the warp's j-th 32 rows (a warp of more than 1024 rows votes twice)
-  const bool votes_kept = per_warp <= 1024;
-  uint32_t my_sure = 0, my_eq = 0;
   int n_sure = 0, n_eq = 0;
-  for (int i0 = w0, j = 0; i0 < w1; i0 += 32, ++j) {
+  for (int e = 0; e < mine; ++e) {
     bool sure, eq;
-    judge(i0 + lane, sure, eq);
-    const uint32_t sb = __ballot_sync(0xffffffffu, sure), eb = __ballot_sync(0xffffffffu, eq);
-    if (lane == j) {
-      my_sure = sb;
-      my_eq = eb;
-    }
-    n_sure += __popc(sb);
-    n_eq += __popc(eb);
+    judge(e, sure, eq);
+    n_sure += sure;
+    n_eq += eq;
   }
-  if (lane == 0) {
-    warp_sum[warp] = n_sure;
-    warp_eq[warp] = n_eq;
+  const int in_sure = warp_scan(n_sure, lane), in_eq = warp_scan(n_eq, lane);
+  __syncthreads();                                              // (warp_sum[0] is read)
+  if (lane == 31) {
+    warp_sum[warp] = in_sure;
+    warp_eq[warp] = in_eq;
   }
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sum[lane], e = warp_eq[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      e += __shfl_xor_sync(0xffffffffu, e, o);
-    }
-    if (lane == 0) {
-      totals[0] = s;
-      totals[1] = e;
-    }
+  int sure_before = warp_prefix(warp_sum, warp, lane) + in_sure - n_sure;
+  int eq_before = warp_prefix(warp_eq, warp, lane) + in_eq - n_eq;
+  if (tid == kSelectThreads - 1) {
+    totals[0] = sure_before + n_sure;
+    totals[1] = eq_before + n_eq;
   }
   ptx::cluster_sync();
-  int sure_before = warp_prefix(warp_sum, warp, lane), eq_before = warp_prefix(warp_eq, warp, lane);
 #pragma unroll
   for (int r = 0; r < kSelectMaxCtas - 1; ++r)
     if (r < rank) {
       sure_before += ld_cluster(totals, r);
       eq_before += ld_cluster(totals + 1, r);
     }
-  for (int i0 = w0, j = 0; i0 < w1; i0 += 32, ++j) {
-    uint32_t sb, eb;
-    if (votes_kept) {
-      sb = __shfl_sync(0xffffffffu, my_sure, j);
-      eb = __shfl_sync(0xffffffffu, my_eq, j);
-    } else {
+  if (n_sure + n_eq > 0)
+    for (int e = 0; e < mine; ++e) {
       bool sure, eq;
-      judge(i0 + lane, sure, eq);
-      sb = __ballot_sync(0xffffffffu, sure);
-      eb = __ballot_sync(0xffffffffu, eq);
+      judge(e, sure, eq);
+      // of the rows with the last key the first `need` stay
+      if (sure || (eq && eq_before < need)) kept[sure_before + min(eq_before, need)] = first + e;
+      sure_before += sure;
+      eq_before += eq;
     }
-    const uint32_t below = (1u << lane) - 1u;
-    // of the rows with the last key the first `need` stay
-    const int eq_rank = eq_before + __popc(eb & below);
-    const int at = sure_before + __popc(sb & below) + min(eq_rank, need);
-    if (((sb >> lane) & 1u) || (((eb >> lane) & 1u) && eq_rank < need)) kept[at] = i0 + lane;
-    sure_before += __popc(sb);
-    eq_before += __popc(eb);
-  }
   ptx::cluster_sync();                                          // no CTA leaves while its counts may be read
 }
 

@@ -363,7 +363,7 @@ lca_status lca_evict_select(lca_plan* p, const float* scores, int64_t score_stri
   sp.stride = score_stride;
   sp.seq_lens = seq_lens;
   sp.B = p->B;
-  sp.cap = std::min<int64_t>(std::min<int64_t>(p->max_L, score_stride), INT32_MAX - 4096);
+  sp.cap = std::min<int64_t>(std::min<int64_t>(p->max_L, score_stride), 1 << 30);
   sp.n_sink = (int)n_sink;
   sp.n_recent = (int)n_recent;
   sp.budget = (int)budget;
@@ -374,7 +374,7 @@ lca_status lca_evict_select(lca_plan* p, const float* scores, int64_t score_stri
   sp.ctas = 1;
   while (sp.ctas < lca::kSelectMaxCtas && sp.cap > 4096LL * sp.ctas) sp.ctas *= 2;
   if (p->B > INT32_MAX / lca::kSelectMaxCtas) return LCA_ERR_UNSUPPORTED;
-  const size_t smem = lca::select_smem(lca::select_run(sp.cap, sp.ctas));
+  const size_t smem = lca::select_smem(lca::select_each(sp.cap, sp.ctas));
   if (!allow_smem<lca::lca_select_kernel>(p->device, lca::select_smem(lca::kSelectKeep))) return LCA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p->B * sp.ctas), 1, 1);
