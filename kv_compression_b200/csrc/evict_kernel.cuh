@@ -262,27 +262,22 @@ struct CompactParams {
   const int32_t* dst0;          // [B]; null: 0
   float* scores;                // [B][score_stride]; null: none
   int64_t score_stride;
-  int strip;                    // 16-byte columns of a block
   int strips_c, strips_k;       // blocks for a row of c, of k; one more for the scores
 };
-
-// The pool row of position `pos`, -1 where its table entry is out of range (the row is then left alone).
-__device__ __forceinline__ int64_t compact_row(const TreeBatch& t, int b, int pos) {
-  if (!t.table) return (int64_t)b * t.page_size + pos;
-  const uint32_t ps = (uint32_t)t.page_size, i = (uint32_t)pos / ps;
-  const int64_t page = t.table[(int64_t)b * t.max_pages + i];
-  if (page < 0 || page >= t.num_pages) {
-    input_error(t.err, 0xB22);
-    return -1;
-  }
-  return page * t.page_size + ((uint32_t)pos - i * ps);
-}
 
 constexpr int kCompactThreads = 256;
 constexpr int kCompactUnroll = 8;
 constexpr int kCompactMaxStrip = 8, kCompactMinStrip = 2;
 
-__global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const CompactParams p) {
+// A row of the list on its way from the list to the copy: its loads are issued a
+// tile apart, so that none is waited for when it is needed.
+struct CompactRow {
+  int s, before;                // src[j], src[j - 1]; s = -1: no such row
+  int page_from, page_to;       // table entries
+};
+
+template <int kStrip>
+__global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const CompactParams p) {
   const TreeBatch& t = p.t;
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int m = p.n_src[b];
@@ -304,10 +299,9 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
     first += (hit - 1) * step + 1;
     span = min(step - 1, end - first);
   }
-  // row j of the list: where it is and where it goes; -1 where it stays put
-  auto check = [&](int j, int& s) {
-    s = src[j];
-    const bool ok = s >= d0 + j && s < t.cap && (j == 0 || s > src[j - 1]);
+  if (first >= m) return;
+  auto valid = [&](int j, int s, int before) {
+    const bool ok = s >= d0 + j && s < t.cap && (j == 0 || s > before);
     if (!ok) input_error(t.err, 0xB21);
     return ok;
   };
@@ -320,8 +314,8 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int j = j0 + u * kCompactThreads + tid;
-        int s = 0;
-        ok[u] = j < m && check(j, s);
+        const int s = j < m ? src[j] : 0;
+        ok[u] = j < m && valid(j, s, j > 0 ? src[j - 1] : -1);
         v[u] = ok[u] ? sc[s] : 0.f;
       }
       __syncthreads();
@@ -342,24 +336,51 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
     base = static_cast<uint8_t*>(const_cast<void*>(t.k));
     row_bytes = t.d_r * p.elem;
   }
-  constexpr int kMaxRows = kCompactThreads / kCompactMinStrip * kCompactUnroll;
-  __shared__ int from_s[2][kMaxRows], to_s[2][kMaxRows];        // pool rows of a tile
-  const int step = kCompactThreads / p.strip;                   // rows a block reads at once
-  const int rows = step * kCompactUnroll;                       // of a tile
-  const int x = tid % p.strip, y = tid / p.strip;
-  const bool act = x < row_bytes / 16 - sx * p.strip;
-  base += (sx * p.strip + x) * 16;
-  auto look_up = [&](int j0, int buf) {
-    for (int i = tid; i < rows; i += kCompactThreads) {
-      const int j = j0 + i;
-      int64_t from = -1, to = -1;
-      int s;
-      if (j < m && check(j, s)) {
-        from = compact_row(t, b, s);
-        to = from < 0 ? -1 : compact_row(t, b, d0 + j);
+  constexpr int kStep = kCompactThreads / kStrip;               // rows a block reads at once
+  constexpr int kRows = kStep * kCompactUnroll;                 // of a tile
+  constexpr int kEach = kRows / kCompactThreads;                // rows a thread looks up
+  __shared__ int from_s[2][kRows], to_s[2][kRows];              // pool rows of a tile; -1: the row is left alone
+  const int x = tid % kStrip, y = tid / kStrip;
+  const bool act = x < row_bytes / 16 - sx * kStrip;
+  base += (sx * kStrip + x) * 16;
+  const uint32_t ps = (uint32_t)t.page_size;
+  const int32_t* table = t.table ? t.table + (int64_t)b * t.max_pages : nullptr;
+  CompactRow r[kEach], nx[kEach];
+  auto list = [&](int j0, CompactRow (&q)[kEach]) {             // the list's entries of the tile at j0
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = j0 + k * kCompactThreads + tid;
+      q[k].s = j < m ? src[j] : -1;
+      q[k].before = j < m && j > 0 ? src[j - 1] : -1;
+    }
+  };
+  auto pages = [&](int j0, CompactRow (&q)[kEach]) {            // their pages' table entries
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int j = j0 + k * kCompactThreads + tid;
+      if (q[k].s >= 0 || j < m) q[k].s = valid(j, q[k].s, q[k].before) ? q[k].s : -1;
+      q[k].page_from = q[k].page_to = b;
+      if (table && q[k].s >= 0) {
+        q[k].page_from = table[(uint32_t)q[k].s / ps];
+        q[k].page_to = table[(uint32_t)(d0 + j) / ps];
       }
-      from_s[buf][i] = (int)from;
-      to_s[buf][i] = (int)to;
+    }
+  };
+  auto rows = [&](int j0, const CompactRow (&q)[kEach], int buf) {   // and their pool rows
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = k * kCompactThreads + tid, to = d0 + j0 + i;
+      int from = -1, dst = -1;
+      if (q[k].s >= 0) {
+        if (table && (q[k].page_from < 0 || q[k].page_from >= t.num_pages || q[k].page_to < 0 || q[k].page_to >= t.num_pages)) {
+          input_error(t.err, 0xB22);
+        } else {
+          from = (int)(q[k].page_from * t.page_size + (uint32_t)q[k].s % ps);
+          dst = (int)(q[k].page_to * t.page_size + (uint32_t)to % ps);
+        }
+      }
+      from_s[buf][i] = from;
+      to_s[buf][i] = dst;
     }
   };
   uint4 v[kCompactUnroll], w[kCompactUnroll];
@@ -367,19 +388,30 @@ __global__ void __launch_bounds__(kCompactThreads) lca_compact_kernel(const Comp
   auto read = [&](int buf, uint4 (&d)[kCompactUnroll], int (&g)[kCompactUnroll]) {
 #pragma unroll
     for (int u = 0; u < kCompactUnroll; ++u) {
-      const int i = u * step + y;
+      const int i = u * kStep + y;
       g[u] = act ? to_s[buf][i] : -1;
       if (g[u] >= 0) d[u] = *reinterpret_cast<const uint4*>(base + (int64_t)from_s[buf][i] * row_bytes);
     }
   };
-  look_up(first, 0);
+  list(first, r);
+  list(first + kRows, nx);
+  pages(first, r);
+  rows(first, r, 0);
+  pages(first + kRows, nx);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) r[k] = nx[k];                 // r: the next tile, its pages under way
+  list(first + 2 * kRows, nx);                                  // nx: the one after it, its list under way
   __syncthreads();
   read(0, v, to);
   int buf = 0;
-  for (int j0 = first; j0 < m; j0 += rows) {
+  for (int j0 = first; j0 < m; j0 += kRows) {
     buf ^= 1;
-    look_up(j0 + rows, buf);
-    __syncthreads();            // this tile's rows are read, the next one's are looked up
+    rows(j0 + kRows, r, buf);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) r[k] = nx[k];
+    pages(j0 + 2 * kRows, r);
+    list(j0 + 3 * kRows, nx);
+    __syncthreads();            // this tile's rows are read, the next one's are known
     read(buf, w, to_w);
 #pragma unroll
     for (int u = 0; u < kCompactUnroll; ++u)

@@ -412,14 +412,17 @@ lca_status lca_cache_compact(lca_plan* p, void* c_pool, void* k_pool, int64_t nu
   cp.dst0 = dst0;
   cp.scores = scores;
   cp.score_stride = score_stride;
-  // the widest strip that still makes a block for each SM
+  // the widest strip that still makes blocks for three quarters of the SMs
   const int64_t cols = (int64_t)(p->d_c + p->d_r) * cp.elem / 16;
-  cp.strip = lca::kCompactMaxStrip;
-  while (cp.strip > lca::kCompactMinStrip && p->B * cols / cp.strip < p->num_sms) cp.strip /= 2;
-  cp.strips_c = (int)ceil_div((int64_t)p->d_c * cp.elem / 16, cp.strip);
-  cp.strips_k = (int)ceil_div((int64_t)p->d_r * cp.elem / 16, cp.strip);
+  int strip = lca::kCompactMaxStrip;
+  while (strip > lca::kCompactMinStrip && p->B * cols / strip < p->num_sms * 3 / 4) strip /= 2;
+  cp.strips_c = (int)ceil_div((int64_t)p->d_c * cp.elem / 16, strip);
+  cp.strips_k = (int)ceil_div((int64_t)p->d_r * cp.elem / 16, strip);
   const dim3 grid((unsigned)(cp.strips_c + cp.strips_k + (scores ? 1 : 0)), (unsigned)p->B);
-  lca::lca_compact_kernel<<<grid, lca::kCompactThreads, 0, static_cast<cudaStream_t>(stream)>>>(cp);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (strip == 8) lca::lca_compact_kernel<8><<<grid, lca::kCompactThreads, 0, s>>>(cp);
+  else if (strip == 4) lca::lca_compact_kernel<4><<<grid, lca::kCompactThreads, 0, s>>>(cp);
+  else lca::lca_compact_kernel<2><<<grid, lca::kCompactThreads, 0, s>>>(cp);
   return launched();
 }
 
