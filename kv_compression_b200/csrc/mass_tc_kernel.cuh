@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         __syncwarp();
         ++ns;
       }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 9; ++c) {
         if (use > 0) ok = ttc::warp_wait(empty + slot, (use - 1) & 1, wt, 0xC41);
         if (!ok) break;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       const bool leaves = u + 1 < u1 && (s.b != b || (kStream && s.tile != tile));   // the operand that stays does not
       const int buf = (int)(i & 1);
       if (i >= 2) ok = ttc::warp_wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43) && ok;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 9; ++c) {
         if (!__all_sync(0xffffffffu, ready)) ok = ttc::warp_wait(full + slot, ph, wt, 0xC44) && ok;
         ptx::tc_fence_after();

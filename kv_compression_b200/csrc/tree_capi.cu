@@ -123,12 +123,13 @@ bool allow_smem(int device, size_t most) {
 
 lca_status launched() { return cudaGetLastError() == cudaSuccess ? LCA_OK : LCA_ERR_CUDA; }
 
-// The merge of the parts, a programmatic dependent of the kernel that wrote them.
-template <typename T>
-lca_status launch_merge(const lca_plan* p, const lca::TreeMergeParams& mp, cudaStream_t stream) {
+// The merge of the parts, a programmatic dependent of the kernel that wrote
+// them; four warps share a run of dims where all CTAs are resident at once.
+template <typename T, int kSplit>
+lca_status launch_merge_split(const lca_plan* p, const lca::TreeMergeParams& mp, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t R = (int64_t)mp.t.T * mp.t.H;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(R, ceil_div(16LL * p->num_sms, mp.t.B)), (unsigned)mp.t.B, 1);
+  const int64_t ctas = (int64_t)mp.t.T * mp.t.H * ceil_div(mp.t.d_c, lca::tree_merge_dims(kSplit));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(ctas, ceil_div(16LL * p->num_sms, mp.t.B)), (unsigned)mp.t.B, 1);
   cfg.blockDim = dim3(lca::kTreeMergeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -136,7 +137,13 @@ lca_status launch_merge(const lca_plan* p, const lca::TreeMergeParams& mp, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lca::lca_tree_merge_kernel<T>, mp) == cudaSuccess ? LCA_OK : LCA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lca::lca_tree_merge_kernel<T, kSplit>, mp) == cudaSuccess ? LCA_OK : LCA_ERR_CUDA;
+}
+
+template <typename T>
+lca_status launch_merge(const lca_plan* p, const lca::TreeMergeParams& mp, cudaStream_t stream) {
+  const int64_t shared = (int64_t)mp.t.B * mp.t.T * mp.t.H * ceil_div(mp.t.d_c, lca::tree_merge_dims(4));
+  return shared <= 8LL * p->num_sms ? launch_merge_split<T, 4>(p, mp, stream) : launch_merge_split<T, 1>(p, mp, stream);
 }
 
 template <typename T>

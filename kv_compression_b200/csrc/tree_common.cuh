@@ -116,26 +116,40 @@ struct TreeMergeParams {
 constexpr int kTreeMergeThreads = 128;
 constexpr int kTreeMaxParts = 1024;
 
-// One CTA per (node, head) row of one sequence; the parts are added in order.
-// Latency is what it costs: every part's (M, Z) is read at once by a thread of
-// its own, and a thread's four dims come from eight parts at a time.
-template <typename T>
+// One CTA per (node, head) row of one sequence and run of its dims: a lane has
+// four of 128, and kSplit warps share those 128, each with every kSplit-th part,
+// eight of them at a time; their sums are added in warp order, so the result
+// does not depend on timing.  Every part's (M, Z) is read at once by a thread of
+// its own.  What it costs is latency: with few rows 4 warps share (82 parts of
+// 64 rows: 49 -> 34 us for the whole call), with rows for several CTAs an SM one
+// warp does it alone and a CTA takes 512 dims (9 parts of 4096 rows: sharing
+// took 25 us more).
+constexpr int tree_merge_dims(int split) { return 128 * (kTreeMergeThreads / 32) / split; }
+
+template <typename T, int kSplit>
 __global__ void __launch_bounds__(kTreeMergeThreads) lca_tree_merge_kernel(const TreeMergeParams p) {
+  constexpr int kWarps = kTreeMergeThreads / 32;
   __shared__ float weight[kTreeMaxParts];
-  __shared__ float2 warp_mz[kTreeMergeThreads / 32];
+  __shared__ float2 warp_mz[kWarps];
+  __shared__ float4 sums[kWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const TreeSplit sp = p.split[b];
   if (!sp.bad && (sp.parts == 0 || (p.direct && sp.parts == 1))) return;
   const TreeLens ln = tree_lens(p.t, b);
   const int64_t R = (int64_t)p.t.T * p.t.H, live = sp.bad ? R : (int64_t)ln.d * p.t.H;
-  const int quads = p.t.d_c / 4;
-  for (int64_t r = blockIdx.x; r < live; r += gridDim.x) {
-    T* out = static_cast<T*>(p.out) + ((int64_t)b * R + r) * p.t.d_c;
-    float* lse = p.lse ? p.lse + (int64_t)b * R + r : nullptr;
+  constexpr int kDims = tree_merge_dims(kSplit);
+  const int chunks = (p.t.d_c + kDims - 1) / kDims, turn = warp % kSplit;
+  for (int64_t g = blockIdx.x; g < live * chunks; g += gridDim.x) {
+    const int64_t r = g / chunks;
+    const int chunk = (int)(g - r * chunks), dim = chunk * kDims + 128 * (warp / kSplit) + 4 * lane;
+    const bool has = dim < p.t.d_c;
+    T* out = static_cast<T*>(p.out) + ((int64_t)b * R + r) * p.t.d_c + dim;
+    float* lse = p.lse && chunk == 0 ? p.lse + (int64_t)b * R + r : nullptr;
     if (sp.bad) {
-      for (int d = tid; d < p.t.d_c; d += kTreeMergeThreads) out[d] = from_f32<T>(__int_as_float(0x7fc00000));
-      if (lse && tid == 0) *lse = __int_as_float(0x7fc00000);
+      const float nan = __int_as_float(0x7fc00000);
+      if (has && turn == 0) store4(out, make_float4(nan, nan, nan, nan));
+      if (lse && tid == 0) *lse = nan;
       continue;
     }
     const int rb = (int)(r / p.rows_per_block), col = (int)(r - (int64_t)rb * p.rows_per_block);
@@ -162,36 +176,43 @@ __global__ void __launch_bounds__(kTreeMergeThreads) lca_tree_merge_kernel(const
     M = -INFINITY;
     Z = 0.f;
 #pragma unroll
-    for (int w = 0; w < kTreeMergeThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float2 mz = warp_mz[w];
       const float top = fmaxf(M, mz.x);
       Z = Z * tree_scale(M, top) + mz.y * tree_scale(mz.x, top);
       M = top;
     }
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    for (int s = tid; s < sp.parts; s += kTreeMergeThreads) weight[s] = tree_scale(weight[s], M) * inv;
-    __syncthreads();
-    for (int q = tid; q < quads; q += kTreeMergeThreads) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float* o = p.part_o + i0 * p.t.d_c + 4 * q;
-      constexpr int kAtOnce = 8;
-      for (int s0 = 0; s0 < sp.parts; s0 += kAtOnce) {
-        float4 v[kAtOnce];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* o = p.part_o + i0 * p.t.d_c + dim;
+    constexpr int kAtOnce = 8;
+    for (int s0 = turn; s0 < sp.parts; s0 += kAtOnce * kSplit) {
+      float4 v[kAtOnce];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-          if (s0 + u < sp.parts) v[u] = *reinterpret_cast<const float4*>(o + (s0 + u) * step * p.t.d_c);
+      for (int u = 0; u < kAtOnce; ++u)
+        if (has && s0 + u * kSplit < sp.parts) v[u] = *reinterpret_cast<const float4*>(o + (s0 + u * kSplit) * step * p.t.d_c);
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-          if (s0 + u < sp.parts) {
-            const float w = weight[s0 + u];
-            acc.x = fmaf(w, v[u].x, acc.x); acc.y = fmaf(w, v[u].y, acc.y);
-            acc.z = fmaf(w, v[u].z, acc.z); acc.w = fmaf(w, v[u].w, acc.w);
-          }
-      }
-      store4(out + 4 * q, acc);
+      for (int u = 0; u < kAtOnce; ++u)
+        if (has && s0 + u * kSplit < sp.parts) {
+          const float w = tree_scale(weight[s0 + u * kSplit], M) * inv;
+          acc.x = fmaf(w, v[u].x, acc.x); acc.y = fmaf(w, v[u].y, acc.y);
+          acc.z = fmaf(w, v[u].z, acc.z); acc.w = fmaf(w, v[u].w, acc.w);
+        }
     }
+    if constexpr (kSplit > 1) {
+      sums[warp][lane] = acc;
+      __syncthreads();
+#pragma unroll
+      for (int w = 1; w < kSplit; ++w) {
+        const float4 v = sums[(warp + w) % kWarps][lane];
+        if (turn == 0) {
+          acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        }
+      }
+    }
+    if (turn == 0 && has) store4(out, acc);
     if (lse && tid == 0) *lse = Z == 0.f ? -INFINITY : kTreeLn2 * (M + log2f(Z));
-    __syncthreads();             // `weight` is free again
+    __syncthreads();             // the shared values are free again
   }
 }
 

@@ -443,28 +443,26 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
           ph ^= 1;
         }
         ++it;
+        if (ptx::elect_one()) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          int slot = here + m;
-          if (slot >= kSlots) slot -= kSlots;
-          if (m == 3) {
-            int parity;
-            uint64_t* ahead = load_bar(0, parity);
-            ready = ptx::mbar_test_wait(ahead, parity);
-          }
-          if (ptx::elect_one()) {
+          for (int m = 0; m < 4; ++m) {
+            int slot = here + m;
+            if (slot >= kSlots) slot -= kSlots;
             const uint64_t a = d_ct + (uint64_t)((slot * kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               ptx::mma_bf16_ss(tmem + kColO + N * m, a + (uint64_t)((2048 * k) >> 4), d_p + (uint64_t)((256 * k) >> 4),
                                kIdO, k > 0 ? 1u : first);
             ptx::mma_commit(empty + slot);
-            if (m == 3) {
-              if (L::kAlias) ptx::mma_commit(k_empty);
-              if (tile + 1 == un.t1) ptx::mma_commit(event);
-            }
           }
-          __syncwarp();
+          if (L::kAlias) ptx::mma_commit(k_empty);
+          if (tile + 1 == un.t1) ptx::mma_commit(event);
+        }
+        __syncwarp();
+        {
+          int parity;
+          uint64_t* ahead = load_bar(0, parity);
+          ready = ptx::mbar_test_wait(ahead, parity);
         }
         if (tile + 1 == un.t1) ++ev;
       }
