@@ -37,10 +37,18 @@ struct Workspace {
   size_t mz, o, bytes;    // offsets, and the whole
 };
 
+// Query rows of a block of the CUDA-core kernels: 32 where there are more than 8 and shared memory holds them
+// beside a tile (d_c + d_r up to about 880).
+int simt_rows(const lca_plan* p, int T) {
+  const bool wide = (int64_t)T * p->H > lca::kTreeSimtRows &&
+                    lca::tree_wide_smem(p->d_c, p->d_r, lca::tree_wide_tokens(p->d_c, p->d_r)) <= kMaxSmem;
+  return wide ? lca::kTreeWideRows : lca::kTreeSimtRows;
+}
+
 // Parts the CUDA-core kernel cuts each sequence into: about four CTAs per SM
-// over B and the blocks of 8 rows; one part writes its output itself.
+// over B and the row blocks; one part writes its output itself.
 int64_t simt_parts(const lca_plan* p, int T) {
-  const int64_t units = (int64_t)p->B * ceil_div((int64_t)T * p->H, lca::kTreeSimtRows);
+  const int64_t units = (int64_t)p->B * ceil_div((int64_t)T * p->H, simt_rows(p, T));
   const int64_t most = std::min<int64_t>(lca::kTreeMaxParts, ceil_div(p->max_L, lca::kTreeSimtTile));
   return std::max<int64_t>(1, std::min<int64_t>(4LL * p->num_sms / units, most));
 }
@@ -57,7 +65,7 @@ int tc_rows(const lca_plan* p, int T) {
 Workspace workspace_of(const lca_plan* p, int T) {
   Workspace w;
   const int64_t parts = simt_parts(p, T);
-  w.slot_rows = parts > 1 ? parts * p->B * round_up((int64_t)T * p->H, lca::kTreeSimtRows) : 0;
+  w.slot_rows = parts > 1 ? parts * p->B * round_up((int64_t)T * p->H, simt_rows(p, T)) : 0;
   if (tc_ok(p)) w.slot_rows = std::max<int64_t>(w.slot_rows, (int64_t)lca::kTreeMaxWaves * p->num_sms * tc_rows(p, T));
   static_assert(sizeof(lca::mtc::Split) <= sizeof(lca::TreeSplit), "one record's room");
   w.mz = (size_t)round_up((int64_t)p->B * sizeof(lca::TreeSplit), 256);
@@ -146,6 +154,15 @@ lca_status launch_merge(const lca_plan* p, const lca::TreeMergeParams& mp, cudaS
   return shared <= 8LL * p->num_sms ? launch_merge_split<T, 4>(p, mp, stream) : launch_merge_split<T, 1>(p, mp, stream);
 }
 
+template <typename T, int kTokens, int kRpt>
+lca_status launch_tree_wide(const lca_plan* p, const lca::TreeSimtParams& sp, dim3 grid, cudaStream_t stream) {
+  const size_t smem = lca::tree_wide_smem(sp.t.d_c, sp.t.d_r, kTokens);
+  if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
+  if (!allow_smem<lca::lca_tree_wide_kernel<T, kTokens, kRpt>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
+  lca::lca_tree_wide_kernel<T, kTokens, kRpt><<<grid, lca::kTreeSimtThreads, smem, stream>>>(sp);
+  return launched();
+}
+
 template <typename T>
 lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c, const void* q_r, void* out,
                          float* lse, uint8_t* ws, const Workspace& w, cudaStream_t stream) {
@@ -159,19 +176,29 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   sp.part_o = reinterpret_cast<float*>(ws + w.o);
   sp.out = out;
   sp.lse = lse;
-  const size_t smem = lca::tree_simt_smem(t.d_c, t.d_r);
-  if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
-  if (!allow_smem<lca::lca_tree_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
-  const dim3 grid((unsigned)sp.n_split, (unsigned)ceil_div((int64_t)t.T * t.H, lca::kTreeSimtRows), (unsigned)t.B);
-  lca::lca_tree_simt_kernel<T><<<grid, lca::kTreeSimtThreads, smem, stream>>>(sp);
-  const lca_status st = launched();
+  const int rows = simt_rows(p, t.T);
+  const dim3 grid((unsigned)sp.n_split, (unsigned)ceil_div((int64_t)t.T * t.H, rows), (unsigned)t.B);
+  lca_status st;
+  if (rows == lca::kTreeSimtRows) {
+    const size_t smem = lca::tree_simt_smem(t.d_c, t.d_r);
+    if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
+    if (!allow_smem<lca::lca_tree_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
+    lca::lca_tree_simt_kernel<T><<<grid, lca::kTreeSimtThreads, smem, stream>>>(sp);
+    st = launched();
+  } else if (lca::tree_wide_tokens(t.d_c, t.d_r) == 64) {
+    st = t.d_c <= 64 ? launch_tree_wide<T, 64, 2>(p, sp, grid, stream) : t.d_c <= 128 ? launch_tree_wide<T, 64, 4>(p, sp, grid, stream)
+                                                                                     : launch_tree_wide<T, 64, 8>(p, sp, grid, stream);
+  } else {
+    st = t.d_c <= 256 ? launch_tree_wide<T, 32, 8>(p, sp, grid, stream) : t.d_c <= 512 ? launch_tree_wide<T, 32, 16>(p, sp, grid, stream)
+                                                                                      : launch_tree_wide<T, 32, 32>(p, sp, grid, stream);
+  }
   if (st != LCA_OK) return st;
   lca::TreeMergeParams mp = {};
   mp.t = t;
   mp.part_o = sp.part_o;
   mp.part_mz = sp.part_mz;
   mp.split = sp.split;
-  mp.rows_per_block = lca::kTreeSimtRows;
+  mp.rows_per_block = rows;
   mp.direct = sp.n_split == 1;
   mp.out = out;
   mp.lse = lse;
@@ -224,11 +251,22 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
 
 template <typename T>
 lca_status run_mass_simt(const lca_plan* p, const lca::MassParams& mp, cudaStream_t stream) {
-  const size_t smem = lca::tree_simt_smem(mp.t.d_c, mp.t.d_r);
+  const int tokens = lca::tree_wide_tokens(mp.t.d_c, mp.t.d_r);
+  const bool narrow = simt_rows(p, mp.t.T) == lca::kTreeSimtRows;
+  const size_t smem = narrow ? lca::tree_simt_smem(mp.t.d_c, mp.t.d_r) : lca::tree_wide_smem(mp.t.d_c, mp.t.d_r, tokens);
   if (smem > kMaxSmem) return LCA_ERR_UNSUPPORTED;
-  if (!allow_smem<lca::lca_mass_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
-  const int64_t blocks = std::min<int64_t>(ceil_div(mp.t.cap, lca::kTreeSimtTile), std::max<int64_t>(1, 8LL * p->num_sms / p->B));
-  lca::lca_mass_simt_kernel<T><<<dim3((unsigned)blocks, (unsigned)p->B), lca::kTreeSimtThreads, smem, stream>>>(mp);
+  const int64_t tiles = ceil_div(mp.t.cap, narrow ? lca::kTreeSimtTile : tokens);
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, std::max<int64_t>(1, 8LL * p->num_sms / p->B)), (unsigned)p->B);
+  if (narrow) {
+    if (!allow_smem<lca::lca_mass_simt_kernel<T>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
+    lca::lca_mass_simt_kernel<T><<<grid, lca::kTreeSimtThreads, smem, stream>>>(mp);
+  } else if (tokens == 64) {
+    if (!allow_smem<lca::lca_mass_wide_kernel<T, 64>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
+    lca::lca_mass_wide_kernel<T, 64><<<grid, lca::kTreeSimtThreads, smem, stream>>>(mp);
+  } else {
+    if (!allow_smem<lca::lca_mass_wide_kernel<T, 32>>(p->device, kMaxSmem)) return LCA_ERR_CUDA;
+    lca::lca_mass_wide_kernel<T, 32><<<grid, lca::kTreeSimtThreads, smem, stream>>>(mp);
+  }
   return launched();
 }
 

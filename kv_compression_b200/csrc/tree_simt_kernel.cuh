@@ -6,9 +6,15 @@
 //   tree    out[r] = sum_t softmax_t(x[r][t]) c_t, lse[r] = log sum_t e^{x[r][t]}
 //   mass    s[t] = decay prev[t] + sum_r e^{x[r][t] - lse[r]}
 //
-// A block holds 32 tokens' rows in shared memory as fp32 and works on 8 rows r
-// at a time: a warp per row and a lane per token for the products and the
-// running maximum and sum; then a thread per latent dim for the sum of values.
+// Up to 8 query rows a sequence: a block holds 32 tokens' rows in shared memory
+// as fp32, with a warp per row and a lane per token for the products and the
+// running maximum and sum, then a thread per latent dim for the sum of values.
+// More: blocks of 32 rows x 64 (wide rows: 32) tokens, both in shared memory; a thread
+// has 2 rows x 4 (2) tokens of the products, 16-byte reads of both sides (6 for 32
+// FMAs), then 4 dims x 2 to 32 rows of the sum of values (3 reads for 32 FMAs at
+// d_c = 256).  Bound by shared memory reads (80% of the FMA rate for the
+// products), and by what its phases leave idle: two or more blocks an SM overlap.
+// Measured (192 rows of 288 dims, 3 x 30334 tokens): 2133 us with 8-row blocks.
 // Tokens that a row does not see are left out of every sum (no 0 x value), so
 // whatever their rows hold is not felt.
 #pragma once
@@ -199,6 +205,182 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
   }
 }
 
+// ---------------------------------------------------------------- blocks of 32 rows
+constexpr int kTreeWideRows = 32;
+
+__host__ __device__ inline size_t tree_wide_smem(int d_c, int d_r, int tokens) {
+  const size_t d = (size_t)d_c + d_r + 4;
+  return sizeof(float) * ((kTreeWideRows + tokens) * d + (size_t)tokens * (kTreeWideRows + 4) + 2 * kTreeWideRows);
+}
+// Tokens of a tile: 64 where two blocks then fit an SM.
+__host__ __device__ inline int tree_wide_tokens(int d_c, int d_r) { return tree_wide_smem(d_c, d_r, 64) <= 113 * 1024 ? 64 : 32; }
+
+// Stage `count` rows of d_c and d_r elements as fp32 rows of d_c + d_r + 4; row(j) gives the j-th row's number or -1 (zeros).
+template <typename T, class Row>
+__device__ __forceinline__ void tree_stage_rows(const void* c, const void* k, int d_c, int d_r, int count, float* dst, Row row) {
+  const int dq = (d_c + d_r) / 4, cq = d_c / 4, stride = d_c + d_r + 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j = warp; j < count; j += kTreeSimtThreads / 32) {
+    const int64_t r = row(j);
+    float* to = dst + (size_t)j * stride;
+    const T* pc = static_cast<const T*>(c) + r * d_c;
+    const T* pk = static_cast<const T*>(k) + r * d_r;
+    for (int i = lane; i < dq; i += 32)
+      *reinterpret_cast<float4*>(to + 4 * i) = r < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : i < cq ? load4(pc + 4 * i) : load4(pk + 4 * (i - cq));
+  }
+}
+
+// Products of query rows 2 ty, 2 ty + 1 with tokens tx, tx + 16, ...
+template <int J>
+__device__ __forceinline__ void tree_products(const float* q, const float* tile, int d, int ty, int tx, float (&acc)[2][J]) {
+  const int stride = d + 4;
+  const float *q0 = q + (size_t)(2 * ty) * stride, *q1 = q0 + stride, *t0 = tile + (size_t)tx * stride;
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[0][j] = acc[1][j] = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < d; i += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(q0 + i), b = *reinterpret_cast<const float4*>(q1 + i);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(t0 + (size_t)(16 * j) * stride + i);
+      acc[0][j] = fmaf(a.x, v.x, acc[0][j]); acc[1][j] = fmaf(b.x, v.x, acc[1][j]);
+      acc[0][j] = fmaf(a.y, v.y, acc[0][j]); acc[1][j] = fmaf(b.y, v.y, acc[1][j]);
+      acc[0][j] = fmaf(a.z, v.z, acc[0][j]); acc[1][j] = fmaf(b.z, v.z, acc[1][j]);
+      acc[0][j] = fmaf(a.w, v.w, acc[0][j]); acc[1][j] = fmaf(b.w, v.w, acc[1][j]);
+    }
+  }
+}
+
+// grid (n_split, ceil(T H / 32), B); kRpt: rows of a thread in the sum of values, 32 / (256 / (d_c / 4)) or more.
+template <typename T, int kTokens, int kRpt>
+__global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const TreeSimtParams p) {
+  constexpr int J = kTokens / 16, kPs = kTreeWideRows + 4;
+  extern __shared__ float tree_smem[];
+  const TreeBatch& t = p.t;
+  const int b = blockIdx.z, rb = blockIdx.y, s = blockIdx.x, tid = threadIdx.x;
+  const int ty = tid >> 4, tx = tid & 15;
+  const int d = t.d_c + t.d_r, stride = d + 4;
+  float* q = tree_smem;
+  float* tile = q + (size_t)kTreeWideRows * stride;
+  float* pw = tile + (size_t)kTokens * stride;                  // [token][row] weights; negative: not seen
+  float* fac = pw + kTokens * kPs;                              // [32] factors of the sums so far
+  const TreeLens ln = tree_lens(t, b);
+  const int slot0 = b * p.n_split * (int)gridDim.y;
+  if (s == 0 && rb == 0 && tid == 0) {
+    p.split[b] = TreeSplit{slot0, ln.d > 0 ? p.n_split : 0, (int)gridDim.y, ln.bad ? 1 : 0};
+    if (ln.bad) input_error(t.err, 0xB01);
+  }
+  const int64_t rows = (int64_t)ln.d * t.H, r0 = (int64_t)rb * kTreeWideRows;
+  if (r0 >= rows) return;
+  const int64_t q0 = (int64_t)b * t.T * t.H + r0;
+  tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, q, [&](int j) { return r0 + j < rows ? q0 + j : (int64_t)-1; });
+  unsigned long long word[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) word[k] = r0 + 2 * ty + k < rows ? tree_word(t, b, (int)((r0 + 2 * ty + k) / t.H)) : 0ull;
+  const int total = ln.n + ln.d;
+  int per = (total + p.n_split - 1) / p.n_split;
+  per = (per + kTokens - 1) / kTokens * kTokens;
+  const int lo = (int)min((int64_t)total, (int64_t)s * per), hi = (int)min((int64_t)total, (int64_t)lo + per);
+  const int groups = t.d_c / 4, g = tid % groups, rg = tid / groups;    // sum of values: 4 dims x kRpt rows
+  const bool act = rg * kRpt < kTreeWideRows;
+  float M[2] = {-INFINITY, -INFINITY}, Z[2] = {0.f, 0.f};
+  float4 acc[kRpt];
+#pragma unroll
+  for (int k = 0; k < kRpt; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t0 = lo; t0 < hi; t0 += kTokens) {
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, tile, [&](int j) { return t0 + j < hi ? tree_row(t, b, t0 + j, 0xB02) : (int64_t)-1; });
+    __syncthreads();
+    float x[2][J];
+    tree_products<J>(q, tile, d, ty, tx, x);
+    const bool special = t0 + kTokens > ln.n || t0 + kTokens > hi;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float top = -INFINITY;
+      uint32_t seen = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int pos = t0 + tx + 16 * j;
+        const bool sees = !special || (pos < hi && tree_sees(ln, word[k], pos));
+        seen |= (uint32_t)sees << j;
+        x[k][j] = sees ? x[k][j] * kTreeLog2e : -INFINITY;
+        top = fmaxf(top, x[k][j]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(M[k], top);
+      const float f = tree_scale(M[k], top);
+      M[k] = top;
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float e = (seen >> j) & 1u ? exp2f(x[k][j] - top) : 0.f;
+        z += e;
+        pw[(tx + 16 * j) * kPs + 2 * ty + k] = (seen >> j) & 1u ? e : -1.f;
+      }
+      Z[k] = Z[k] * f + z;
+      if (tx == 0) fac[2 * ty + k] = f;
+    }
+    __syncthreads();
+    if (act) {
+#pragma unroll
+      for (int k = 0; k < kRpt; ++k) {
+        const float f = fac[rg * kRpt + k];
+        acc[k].x *= f; acc[k].y *= f; acc[k].z *= f; acc[k].w *= f;
+      }
+      const int tokens = min(kTokens, hi - t0);
+      const float* vp = tile + 4 * g;
+      const float* wp = pw + rg * kRpt;
+      for (int j = 0; j < tokens; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(vp + (size_t)j * stride);
+#pragma unroll
+        for (int k = 0; k < kRpt; ++k) {
+          const float e = wp[j * kPs + k];
+          if (!special || !(e < 0.f)) {
+            acc[k].x = fmaf(e, v.x, acc[k].x); acc[k].y = fmaf(e, v.y, acc[k].y);
+            acc[k].z = fmaf(e, v.z, acc[k].z); acc[k].w = fmaf(e, v.w, acc[k].w);
+          }
+        }
+      }
+    }
+  }
+  // a row's Z over its 16 lanes; then the rows' factors or statistics
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) Z[k] += __shfl_xor_sync(0xffffffffu, Z[k], o);
+  }
+  const int64_t i0 = (int64_t)(slot0 + s * (int)gridDim.y + rb) * kTreeWideRows;
+  __syncthreads();
+  if (tx == 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = r0 + 2 * ty + k;
+      fac[2 * ty + k] = Z[k] == 0.f ? 0.f : 1.f / Z[k];
+      if (r >= rows) continue;
+      if (p.n_split > 1) {
+        p.part_mz[2 * (i0 + 2 * ty + k)] = M[k];
+        p.part_mz[2 * (i0 + 2 * ty + k) + 1] = Z[k];
+      } else if (p.lse) {
+        p.lse[(int64_t)b * t.T * t.H + r] = Z[k] == 0.f ? -INFINITY : kTreeLn2 * (M[k] + log2f(Z[k]));
+      }
+    }
+  }
+  __syncthreads();
+  if (!act) return;
+#pragma unroll
+  for (int k = 0; k < kRpt; ++k) {
+    const int r = rg * kRpt + k;
+    if (r0 + r >= rows) break;
+    if (p.n_split > 1) {
+      store4(p.part_o + (i0 + r) * t.d_c + 4 * g, acc[k]);
+    } else {
+      const float f = fac[r];
+      store4(static_cast<T*>(p.out) + (q0 + r) * t.d_c + 4 * g, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
+    }
+  }
+}
+
 struct MassParams {
   TreeBatch t;
   const void* q_c;
@@ -258,6 +440,58 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_simt_kernel(const M
 #pragma unroll
       for (int w = 0; w < kTreeSimtRows; ++w) s += part[w * kTreeSimtTile + lane];
       mass_store(p, b, pos, ln.n, s);
+    }
+  }
+}
+
+// The same in tiles of kTokens tokens and blocks of 32 rows.
+template <typename T, int kTokens>
+__global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_wide_kernel(const MassParams p) {
+  constexpr int J = kTokens / 16;
+  extern __shared__ float tree_smem[];
+  const TreeBatch& t = p.t;
+  const int b = blockIdx.y, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int d = t.d_c + t.d_r, stride = d + 4;
+  float* q = tree_smem;
+  float* tile = q + (size_t)kTreeWideRows * stride;
+  float* part = tile + (size_t)kTokens * stride;                // [16][kTokens]
+  const TreeLens ln = tree_lens(t, b);
+  if (ln.bad && blockIdx.x == 0 && tid == 0) input_error(t.err, 0xB03);
+  const int64_t rows = (int64_t)ln.d * t.H, q0 = (int64_t)b * t.T * t.H;
+  const int total = ln.n + ln.d;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < total; t0 += (int64_t)gridDim.x * kTokens) {
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, tile, [&](int j) { return t0 + j < total ? tree_row(t, b, (int)t0 + j, 0xB04) : (int64_t)-1; });
+    const bool special = t0 + kTokens > ln.n;
+    float sum[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) sum[j] = 0.f;
+    for (int64_t r0 = 0; r0 < rows; r0 += kTreeWideRows) {
+      __syncthreads();
+      tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, q, [&](int j) { return r0 + j < rows ? q0 + r0 + j : (int64_t)-1; });
+      __syncthreads();
+      float x[2][J];
+      tree_products<J>(q, tile, d, ty, tx, x);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t r = r0 + 2 * ty + k;
+        if (r >= rows) continue;
+        const float off = mass_offset(p.lse[q0 + r]);
+        if (off == INFINITY) continue;
+        const unsigned long long word = special ? tree_word(t, b, (int)(r / t.H)) : 0ull;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (!special || tree_sees(ln, word, (int)t0 + tx + 16 * j)) sum[j] += exp2f(fmaf(x[k][j], kTreeLog2e, -off));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) part[ty * kTokens + tx + 16 * j] = sum[j];
+    __syncthreads();
+    if (tid < kTokens && t0 + tid < total) {
+      float a = 0.f;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) a += part[w * kTokens + tid];
+      mass_store(p, b, (int)t0 + tid, ln.n, a);
     }
   }
 }

@@ -152,6 +152,11 @@ SMALL = [
     (6, 4, [100, 511], None, 128, "bf16", 128, 32),
     (1, 3, [50], None, 0, "bf16", 1024, 256),
     (2, 5, [77, 1], None, 0, "f32", 8, 8),
+    (6, 12, [300, 0, 65], [12, 7, 1], 64, "bf16", 256, 32),
+    (16, 4, [129, 64], None, 0, "f32", 40, 24),
+    (4, 5, [70], None, 0, "f32", 512, 128),
+    (10, 1, [33, 200], None, 64, "bf16", 640, 64),
+    (3, 11, [90], None, 0, "f32", 1024, 256),
 ]
 IDS = ["H{}_T{}_n{}_d{}_p{}_{}_{}_{}".format(a, b, "-".join(map(str, c)), "" if d is None else "-".join(map(str, d)), e, f, g, h)
        for a, b, c, d, e, f, g, h in SMALL]
