@@ -15,7 +15,12 @@
 //   up to 128 rows   the queries stay (N = 16 .. 128) and the cache streams: it is read
 //                    once, at memory speed
 //   more rows        a tile of the cache stays and the query blocks (N = 128) stream, from
-//                    L2: the cache comes from memory once whatever the number of rows
+//                    L2: the cache comes from memory once whatever the number of rows.
+//                    Shared memory would bound this: an MMA of 64 cycles reads 8 KB of
+//                    operands there (all of its 128 bytes a cycle) while 4 KB of
+//                    queries arrive.  So the tile's C is copied into tensor memory
+//                    (256 columns, a token's row in its lane) and is the A operand from
+//                    there; K (64 of 576 dims) stays in shared memory.
 // A tile whose row blocks are split over CTAs gets one partial sum from each;
 // lca_mass_finish_kernel adds those in CTA order, so the result does not depend
 // on timing.
@@ -36,24 +41,30 @@ using ttc::Wait;
 constexpr int kAddWarps = 8;
 constexpr int kThreads = 32 * (2 + kAddWarps);
 constexpr int kBarAdd = 1;
-constexpr int kMaxSlots = 12;
+constexpr int kMaxSlots = 5;
+constexpr uint32_t kColA = 256;      // the tile's C in TMEM: 32 columns for 64 dims
 
 template <int N, bool kStream>       // kStream: the queries stream
 struct Layout {
   static_assert(!kStream || N == 128, "streamed queries come 128 rows at a time");
   static constexpr int kQChunk = N * 128;
-  static constexpr int kStay = kStream ? kChunk : kQChunk;                 // a chunk of the operand that stays
-  static constexpr int kSlots = N == 128 ? 5 : N == 64 ? 9 : N == 32 ? 11 : 12;
-  static constexpr int kOffRing = 9 * kStay;
-  static constexpr int kOffOff = kOffRing + kSlots * kChunk;               // float [2][N] offsets of the rows
+  static constexpr int kStay = kStream ? kChunk : 9 * kQChunk;             // what stays in shared memory: a tile's K, or Q
+  // The ring: slots of three chunks, three of them, so that a step's slots are always the same ones; beside 128
+  // rows of queries slots of one chunk.  (A load, a barrier and a release for each single chunk set the pace
+  // elsewhere: 430 cycles a chunk for the loading warp, 400 for the MMA warp, where the MMAs take 256.)
+  static constexpr int kPer = N == 128 && !kStream ? 1 : 3;
+  static constexpr int kSlots = kPer == 1 ? 5 : 3;
+  static constexpr int kSlot = kPer * kChunk;
+  static constexpr int kOffRing = kStay;
+  static constexpr int kOffOff = kOffRing + kSlots * kSlot;               // float [2][N] offsets of the rows
   static constexpr int kOffPart = kOffOff + 8 * N;                         // float [128]
   static constexpr int kOffGap = kOffPart + 512;                           // u32 [2][4] rows that add nothing
   static constexpr int kOffBar = kOffGap + 32;
-  static constexpr int kBars = 2 * kMaxSlots + 7;
+  static constexpr int kBars = 2 * kMaxSlots + 8;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr uint32_t kCols = N <= 16 ? 32 : N == 32 ? 64 : N == 64 ? 128 : 256;
+  static constexpr uint32_t kCols = kStream ? 512 : N <= 16 ? 32 : N == 32 ? 64 : N == 64 ? 128 : 256;
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
 
@@ -82,14 +93,14 @@ struct Step {
 template <int N, bool kStream>
 __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_constant__ Params p) {
   using L = Layout<N, kStream>;
-  constexpr int kSlots = L::kSlots;
+  constexpr int kSlots = L::kSlots, kPer = L::kPer, kFills = 9 / kPer;   // slots filled for a step
   constexpr int C = N / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t *full = bars, *empty = bars + kMaxSlots, *stay_full = bars + 2 * kMaxSlots, *stay_empty = stay_full + 1,
-           *s_full = stay_full + 2, *s_empty = stay_full + 4, *drain = stay_full + 6;
+           *s_full = stay_full + 2, *s_empty = stay_full + 4, *drain = stay_full + 6, *a_full = stay_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   const TreeBatch& t = p.m.t;
@@ -108,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       ptx::mbar_init(s_empty + i, kAddWarps);
     }
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(a_full, kAddWarps);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
   }
@@ -196,31 +208,20 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       auto load_q = [&](uint8_t* dst, int c, uint64_t* bar) {
         ptx::tma_load_2d(dst, c < 8 ? &p.tm_qc : &p.tm_qr, c < 8 ? 64 * c : 0, qrow, bar);
       };
-      if (b != last_b || (kStream && tile != last_tile)) {
-        last_b = b;
-        last_tile = tile;
-        if (ns > 0) ok = ttc::warp_wait(stay_empty, (ns - 1) & 1, wt, 0xC40);
-        if (!ok) break;
-        if (ptx::elect_one()) {
-          ptx::mbar_arrive_expect_tx(stay_full, 9 * L::kStay);
-#pragma unroll
-          for (int c = 0; c < 9; ++c) {
-            if constexpr (kStream) load_tile(smem + c * L::kStay, c, stay_full);
-            else load_q(smem + c * L::kStay, c, stay_full);
-          }
-        }
-        __syncwarp();
-        ++ns;
-      }
-#pragma unroll 1
-      for (int c = 0; c < 9; ++c) {
+      // chunks kPer f .. of the tile (up to `count`) or of the queries into the ring
+      auto fill = [&](bool tiles, int f, int count) {
         if (use > 0) ok = ttc::warp_wait(empty + slot, (use - 1) & 1, wt, 0xC41);
-        if (!ok) break;
+        if (!ok) return;
         if (!skip && ptx::elect_one()) {
-          ptx::mbar_arrive_expect_tx(full + slot, kChunk);
-          uint8_t* dst = smem + L::kOffRing + slot * kChunk;
-          if constexpr (kStream) load_q(dst, c, full + slot);
-          else load_tile(dst, c, full + slot);
+          ptx::mbar_arrive_expect_tx(full + slot, min(kPer, count - kPer * f) * kChunk);
+          uint8_t* dst = smem + L::kOffRing + slot * L::kSlot;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int c = kPer * f + k;
+            if (c >= count) break;
+            if (tiles) load_tile(dst + k * kChunk, c, full + slot);
+            else load_q(dst + k * kChunk, c, full + slot);
+          }
         }
         __syncwarp();
         if (!skip && use == 0) sent |= 1 << slot;
@@ -229,7 +230,30 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
           slot = 0;
           ++use;
         }
+      };
+      if (b != last_b || (kStream && tile != last_tile)) {
+        last_b = b;
+        last_tile = tile;
+        if constexpr (kStream) {
+#pragma unroll 1
+          for (int f = 0; f < kFills && ok; ++f) fill(true, f, 8);       // on its way to TMEM
+        }
+        if (ok && ns > 0) ok = ttc::warp_wait(stay_empty, (ns - 1) & 1, wt, 0xC40);
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(stay_full, L::kStay);
+          if constexpr (kStream) {
+            load_tile(smem, 8, stay_full);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 9; ++c) load_q(smem + c * L::kQChunk, c, stay_full);
+          }
+        }
+        __syncwarp();
+        ++ns;
       }
+#pragma unroll 1
+      for (int f = 0; f < kFills && ok; ++f) fill(!kStream, f, 9);
       r0 = n0;
       r1 = n1;
     }
@@ -257,6 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         last_b = s.b;
         last_tile = s.tile;
         ok = ttc::warp_wait(stay_full, ns & 1, wt, 0xC42);
+        if constexpr (kStream) {                       // a round of the ring went to TMEM
+          ok = ok && ttc::warp_wait(a_full, ns & 1, wt, 0xC46);
+          ready = false;
+          ph ^= 1;
+        }
         ++ns;
       }
       const int b = s.b, tile = s.tile;
@@ -264,26 +293,30 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       const bool leaves = u + 1 < u1 && (s.b != b || (kStream && s.tile != tile));   // the operand that stays does not
       const int buf = (int)(i & 1);
       if (i >= 2) ok = ttc::warp_wait(s_empty + buf, (uint32_t)((i >> 1) - 1) & 1, wt, 0xC43) && ok;
-#pragma unroll 1
-      for (int c = 0; c < 9; ++c) {
-        if (!__all_sync(0xffffffffu, ready)) ok = ttc::warp_wait(full + slot, ph, wt, 0xC44) && ok;
+#pragma unroll
+      for (int f = 0; f < kFills; ++f) {
+        const int at = kSlots == kFills ? f : slot;
+        if (!__all_sync(0xffffffffu, ready)) ok = ttc::warp_wait(full + at, ph, wt, 0xC44) && ok;
         ptx::tc_fence_after();
-        int ahead = slot + 1, aph = ph;
-        if (ahead == kSlots) {
-          ahead = 0;
-          aph ^= 1;
-        }
+        const int ahead = at + 1 == kSlots ? 0 : at + 1, aph = at + 1 == kSlots ? ph ^ 1 : ph;
         ready = ptx::mbar_test_wait(full + ahead, aph);
         if (!ok) break;
         if (ptx::elect_one()) {
-          const uint64_t a = d_stay + (uint64_t)((c * L::kStay) >> 4);
-          const uint64_t r = d_ring + (uint64_t)((slot * kChunk) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_bf16_ss(tmem + N * buf, (kStream ? a : r) + (uint64_t)((32 * k) >> 4),
-                             (kStream ? r : a) + (uint64_t)((32 * k) >> 4), kId, (c | k) != 0);
-          ptx::mma_commit(empty + slot);
-          if (c == 8) {
+          for (int j = 0; j < kPer; ++j) {
+            const int c = kPer * f + j;
+            const uint64_t r = d_ring + (uint64_t)((at * L::kSlot + j * kChunk) >> 4);
+            const uint64_t q = d_stay + (uint64_t)((kStream ? 0 : c * L::kQChunk) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t o = (uint64_t)((32 * k) >> 4);
+              if constexpr (!kStream) ptx::mma_bf16_ss(tmem + N * buf, r + o, q + o, kId, (c | k) != 0);
+              else if (c < 8) ptx::mma_bf16_ts(tmem + N * buf, tmem + kColA + 32 * c + 8 * k, r + o, kId, (c | k) != 0);
+              else ptx::mma_bf16_ss(tmem + N * buf, q + o, r + o, kId, 1u);
+            }
+          }
+          ptx::mma_commit(empty + at);
+          if (f == kFills - 1) {
             ptx::mma_commit(s_full + buf);
             if (leaves) ptx::mma_commit(stay_empty);
           }
@@ -331,8 +364,40 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     };
     float o_next = u0 < u1 ? offset(s, l.d) : INFINITY;
     unsigned long long vis = ~0ull;                    // the nodes that see this thread's token
+    int64_t rounds = 0;                                // of the ring
     for (int64_t u = u0; u < u1; ++u, ++i) {
       const int buf = (int)(i & 1);
+      bool live = true;
+      if constexpr (kStream) {
+        if (fresh) {
+          // the tile's C from a round of the ring into TMEM, every other chunk by each half of the warps; the MMAs
+          // that read the last one are done (their last step has been added up)
+#pragma unroll 1
+          for (int f = 0; f < kFills; ++f) {
+            live = ttc::warp_wait(full + f, (uint32_t)rounds & 1, wt, 0xC47) && live;
+#pragma unroll 1
+            for (int c = kPer * f; c < min(8, kPer * f + kPer); ++c) {
+              if ((c & 1) != half) continue;
+              const uint8_t* from = smem + L::kOffRing + c * kChunk + tok * 128;
+              float v[32];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {            // the 16-byte units of a row are swizzled by its number
+                const float4 w = *reinterpret_cast<const float4*>(from + ((j ^ (tok & 7)) << 4));
+                v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
+              }
+              ptx::tmem_st32(tmem + ((uint32_t)(32 * quarter) << 16) + kColA + 32 * c, v);
+            }
+            ptx::named_bar_sync(kBarAdd, 32 * kAddWarps);          // the slot is read
+            if (sid == 0) ptx::mbar_arrive(empty + f);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(a_full);
+          ++rounds;
+        }
+        ++rounds;
+      }
       const int pos0 = s.tile * kTreeTile;
       const bool special = pos0 + kTreeTile > l.n;     // drafted tokens, or the end, in this tile
       if (sid < N) off[buf * N + sid] = o_next;
@@ -352,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
           for (int j = 0; j < lat.d; ++j) vis |= ((tree_word(t, at.b, j) >> node) & 1ull) << j;
       }
       fresh = false;
-      const bool live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45);
+      live = ttc::warp_wait(s_full + buf, (uint32_t)(i >> 1) & 1, wt, 0xC45) && live;
       if (ptx::named_bar_or(kBarAdd, 32 * kAddWarps, !live)) break;
       ptx::tc_fence_after();
       float a0 = 0.f, a1 = 0.f;

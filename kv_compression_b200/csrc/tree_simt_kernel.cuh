@@ -14,7 +14,7 @@
 // FMAs), then 4 dims x 2 to 32 rows of the sum of values (3 reads for 32 FMAs at
 // d_c = 256).  Bound by shared memory reads (80% of the FMA rate for the
 // products), and by what its phases leave idle: two or more blocks an SM overlap.
-// Measured (192 rows of 288 dims, 3 x 30334 tokens): 2133 us with 8-row blocks.
+// Measured (192 rows over 3 x 30334 tokens, bf16): 393 us, against 2134 us with 8-row blocks.
 // Tokens that a row does not see are left out of every sum (no 0 x value), so
 // whatever their rows hold is not felt.
 #pragma once
