@@ -1,7 +1,7 @@
 // mass_tc_kernel.cuh -- accumulated attention weights with tcgen05 tensor cores
 // (bf16, d_c = 512, d_r = 64).
 //
-//   s[t] = decay prev[t] + sum_r 2^{(q[r] . [c_t | k_t]) log2 e - lse[r] log2 e}
+//   s[t] = decay prev[t] + sum_r 2^{(q[r] . [c_t | k_t] - lse[r]) log2 e}
 //
 // Work is a list of (sequence, 128-token tile, block of N query rows), row
 // blocks fastest, and each CTA takes one contiguous range of it.  A step is
@@ -357,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
     bool from_start = s.rb == 0, fresh = true;
     float acc = 0.f;
     TreeLens l = lens_of(s.b);
-    // a row's offset; rows that add nothing have an infinite one.  Read a step ahead.
+    // a row's -lse; rows that add nothing have -inf.  Read a step ahead.
     auto offset = [&](const Step& at, int d) {
       const int r = at.rb * N + sid;
-      return sid < N && r < d * t.H ? mass_offset(p.m.lse[(int64_t)at.b * t.T * t.H + r]) : INFINITY;
+      return sid < N && r < d * t.H ? mass_offset(p.m.lse[(int64_t)at.b * t.T * t.H + r]) : -INFINITY;
     };
-    float o_next = u0 < u1 ? offset(s, l.d) : INFINITY;
+    float o_next = u0 < u1 ? offset(s, l.d) : -INFINITY;
     unsigned long long vis = ~0ull;                    // the nodes that see this thread's token
     int64_t rounds = 0;                                // of the ring
     for (int64_t u = u0; u < u1; ++u, ++i) {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
       const int pos0 = s.tile * kTreeTile;
       const bool special = pos0 + kTreeTile > l.n;     // drafted tokens, or the end, in this tile
       if (sid < N) off[buf * N + sid] = o_next;
-      const uint32_t empty_rows = __ballot_sync(0xffffffffu, o_next == INFINITY);
+      const uint32_t empty_rows = __ballot_sync(0xffffffffu, o_next == -INFINITY);
       if (sid < N && lane == 0) gap[4 * buf + sw] = empty_rows;
       const Step at = s;
       const TreeLens lat = l;
@@ -444,19 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
           }
 #pragma unroll
           for (int c = 0; c < W; ++c) x[c] = (sees >> c) & 1u ? x[c] : -INFINITY;
-          if (gaps != 0u) {                            // -inf - inf: an offset that stands for nothing is passed over
-#pragma unroll
-            for (int c = 0; c < W; ++c) a0 += (sees >> c) & 1u ? ttc::ex2(fmaf(x[c], kTreeLog2e, -o[c])) : 0.f;
-            continue;
-          }
         }
+        const uint64_t log2e = ptx::f32x2(kTreeLog2e, kTreeLog2e);
 #pragma unroll
         for (int c = 0; c < W; c += 4) {
           const float4 o4 = *reinterpret_cast<const float4*>(o + c);
-          a0 += ttc::ex2(fmaf(x[c], kTreeLog2e, -o4.x));
-          a1 += ttc::ex2(fmaf(x[c + 1], kTreeLog2e, -o4.y));
-          a0 += ttc::ex2(fmaf(x[c + 2], kTreeLog2e, -o4.z));
-          a1 += ttc::ex2(fmaf(x[c + 3], kTreeLog2e, -o4.w));
+          float e0, e1, e2, e3;
+          ptx::f32x2_split(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(o4.x, o4.y)), log2e), e0, e1);
+          ptx::f32x2_split(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(x[c + 2], x[c + 3]), ptx::f32x2(o4.z, o4.w)), log2e), e2, e3);
+          a0 += ttc::ex2(e0);
+          a1 += ttc::ex2(e1);
+          a0 += ttc::ex2(e2);
+          a1 += ttc::ex2(e3);
         }
       }
       ptx::tc_fence_before();

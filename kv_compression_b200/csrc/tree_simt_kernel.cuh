@@ -392,8 +392,10 @@ struct MassParams {
   float decay;
 };
 
-// The row's exponent offset: an infinite lse marks a row that adds nothing.
-__device__ __forceinline__ float mass_offset(float lse) { return isinf(lse) ? INFINITY : lse * kTreeLog2e; }
+// -lse of a row; an infinite lse marks a row that adds nothing, and -inf makes it so.  A weight is
+// 2^{(x - lse) log2 e}: the difference is taken first, since lse log2 e alone would be rounded by up to
+// 1e-6 where lse is above 11, and the weight with it.
+__device__ __forceinline__ float mass_offset(float lse) { return isinf(lse) ? -INFINITY : -lse; }
 
 // A position's new sum: cached tokens go on from what they had, drafted ones begin.
 __device__ __forceinline__ void mass_store(const MassParams& p, int b, int pos, int n, float add) {
@@ -430,8 +432,8 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_simt_kernel(const M
       const int64_t r = r0 + warp;
       if (r >= rows) continue;
       const float off = mass_offset(p.lse[(int64_t)b * t.T * t.H + r]);
-      if (off != INFINITY && pos < total && tree_sees(ln, tree_word(t, b, (int)(r / t.H)), pos))
-        sum += exp2f(fmaf(tree_dot(q + (size_t)warp * d, tile + (size_t)lane * stride, d), kTreeLog2e, -off));
+      if (off != -INFINITY && pos < total && tree_sees(ln, tree_word(t, b, (int)(r / t.H)), pos))
+        sum += exp2f((tree_dot(q + (size_t)warp * d, tile + (size_t)lane * stride, d) + off) * kTreeLog2e);
     }
     part[warp * kTreeSimtTile + lane] = sum;
     __syncthreads();
@@ -477,11 +479,11 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_wide_kernel(const M
         const int64_t r = r0 + 2 * ty + k;
         if (r >= rows) continue;
         const float off = mass_offset(p.lse[q0 + r]);
-        if (off == INFINITY) continue;
+        if (off == -INFINITY) continue;
         const unsigned long long word = special ? tree_word(t, b, (int)(r / t.H)) : 0ull;
 #pragma unroll
         for (int j = 0; j < J; ++j)
-          if (!special || tree_sees(ln, word, (int)t0 + tx + 16 * j)) sum[j] += exp2f(fmaf(x[k][j], kTreeLog2e, -off));
+          if (!special || tree_sees(ln, word, (int)t0 + tx + 16 * j)) sum[j] += exp2f((x[k][j] + off) * kTreeLog2e);
       }
     }
 #pragma unroll
