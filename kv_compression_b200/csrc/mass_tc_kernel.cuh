@@ -445,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
 #pragma unroll
           for (int c = 0; c < W; ++c) x[c] = (sees >> c) & 1u ? x[c] : -INFINITY;
         }
-        const uint64_t log2e = ptx::f32x2(kTreeLog2e, kTreeLog2e);
+        const uint64_t log2e = ptx::f32x2(kTreeLog2e, kTreeLog2e), scale = ptx::f32x2(ttc::kLogitScale, ttc::kLogitScale);
 #pragma unroll
         for (int c = 0; c < W; c += 4) {
           const float4 o4 = *reinterpret_cast<const float4*>(o + c);
           float e0, e1, e2, e3;
-          ptx::f32x2_split(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(o4.x, o4.y)), log2e), e0, e1);
-          ptx::f32x2_split(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(x[c + 2], x[c + 3]), ptx::f32x2(o4.z, o4.w)), log2e), e2, e3);
+          ptx::f32x2_split(ptx::mul_f32x2(ptx::fma_f32x2(ptx::f32x2(x[c], x[c + 1]), scale, ptx::f32x2(o4.x, o4.y)), log2e), e0, e1);
+          ptx::f32x2_split(ptx::mul_f32x2(ptx::fma_f32x2(ptx::f32x2(x[c + 2], x[c + 3]), scale, ptx::f32x2(o4.z, o4.w)), log2e), e2, e3);
           a0 += ttc::ex2(e0);
           a1 += ttc::ex2(e1);
           a0 += ttc::ex2(e2);
