@@ -117,23 +117,9 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _refuse(what: str, t, dtype, shape) -> None:
+def _refuse(what: str, t, dtype, shape, device) -> None:
     raise LcaError(LCA_ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}; "
-                   f"wanted a contiguous CUDA tensor of {dtype} {shape}")
-
-
-def _expect(what: str, t, dtype, shape) -> int:
-    """The address of `t`, a contiguous CUDA tensor of this type and shape; LCA_ERR_INVALID_ARG if it is none."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
-        _refuse(what, t, dtype, shape)
-    return t.data_ptr()
-
-
-def _expect_rows(what: str, t, dtype, rows: int) -> int:
-    """The same for a matrix of `rows` rows of any length."""
-    if not (t.dtype is dtype and t.dim() == 2 and t.shape[0] == rows and t.is_contiguous() and t.is_cuda):
-        _refuse(what, t, dtype, (rows, "*"))
-    return t.data_ptr()
+                   f"wanted a contiguous tensor of {dtype} {shape} on cuda:{device}")
 
 
 def _stream_handle(stream) -> int | None:
@@ -278,24 +264,41 @@ class Plan:
         """The handle of `stream`, or of the current one of the plan's device."""
         return self._raw_stream(self._device) if stream is None else stream.cuda_stream
 
+    def _expect(self, what: str, t, dtype, shape) -> int:
+        """The address of `t`, a contiguous tensor of this type and shape on the plan's device; LCA_ERR_INVALID_ARG
+        if it is none."""
+        if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == self._device):
+            _refuse(what, t, dtype, shape, self._device)
+        return t.data_ptr()
+
+    def _expect_rows(self, what: str, t, dtype, rows: int) -> int:
+        """The same for a matrix of `rows` rows of any length."""
+        if not (t.dtype is dtype and t.dim() == 2 and t.shape[0] == rows and t.is_contiguous()
+                and t.get_device() == self._device):
+            _refuse(what, t, dtype, (rows, "*"), self._device)
+        return t.data_ptr()
+
     def _cache_args(self, c_pool, k_pool, page_size: int, block_table):
         """The cache arguments of the C calls, checked: pools [rows, d] (or [B, capacity, d]) and an int32
         block_table [B, max_pages], or None for a contiguous cache with page_size rows a sequence."""
-        if c_pool.dim() == 3:
-            c_pool, k_pool = c_pool.flatten(0, 1), k_pool.flatten(0, 1)
         rows = c_pool.shape[0]
-        c, k = _expect("c_pool", c_pool, self._elem, (rows, self.d_c)), _expect("k_pool", k_pool, self._elem, (rows, self.d_r))
+        if c_pool.dim() == 3:
+            rows *= c_pool.shape[1]
+            for what, t, d in (("c_pool", c_pool, self.d_c), ("k_pool", k_pool, self.d_r)):
+                self._expect(what, t, self._elem, (*c_pool.shape[:2], d))
+            c_pool, k_pool = c_pool.view(rows, self.d_c), k_pool.view(rows, self.d_r)
+        c, k = self._expect("c_pool", c_pool, self._elem, (rows, self.d_c)), self._expect("k_pool", k_pool, self._elem, (rows, self.d_r))
         pages = rows // page_size if page_size > 0 else 0
         if block_table is None:
             return c, k, pages, page_size, None, 1
-        return c, k, pages, page_size, _expect_rows("block_table", block_table, self._i32, self.B), block_table.shape[1]
+        return c, k, pages, page_size, self._expect_rows("block_table", block_table, self._i32, self.B), block_table.shape[1]
 
     def _draft_args(self, q_c, q_r, seq_lens, draft_lens, mask):
         B, T, i32 = self.B, q_c.shape[1], self._i32
-        return (T, _expect("q_c", q_c, self._elem, (B, T, self.H, self.d_c)),
-                _expect("q_r", q_r, self._elem, (B, T, self.H, self.d_r)), _expect("seq_lens", seq_lens, i32, (B,)),
-                None if draft_lens is None else _expect("draft_lens", draft_lens, i32, (B,)),
-                None if mask is None else _expect("mask", mask, self._i64, (B, T)))
+        return (T, self._expect("q_c", q_c, self._elem, (B, T, self.H, self.d_c)),
+                self._expect("q_r", q_r, self._elem, (B, T, self.H, self.d_r)), self._expect("seq_lens", seq_lens, i32, (B,)),
+                None if draft_lens is None else self._expect("draft_lens", draft_lens, i32, (B,)),
+                None if mask is None else self._expect("mask", mask, self._i64, (B, T)))
 
     def tree_workspace(self, n_draft: int, stream=None):
         """A workspace for tree_decode and attn_mass with up to n_draft drafted tokens a sequence: keep one per
@@ -304,16 +307,16 @@ class Plan:
         size = int(self._lib.lca_tree_workspace(self._h, n_draft))
         if size < 0:
             raise LcaError(LCA_ERR_INVALID_ARG, f"tree_workspace: n_draft {n_draft} outside 1 .. {MAX_DRAFT}")
-        ws = torch.empty(size, dtype=torch.uint8, device=self._device)
-        if stream is not None:
-            ws.record_stream(stream)
-        return ws
+        if stream is None:
+            return torch.empty(size, dtype=torch.uint8, device=self._device)
+        with torch.cuda.stream(stream):      # of that stream's memory: free for its next use in that stream's order
+            return torch.empty(size, dtype=torch.uint8, device=self._device)
 
     def _workspace(self, workspace, T: int, stream) -> tuple[int, int]:
         if workspace is None:
             workspace = self.tree_workspace(T, stream)
-        elif not (workspace.is_cuda and workspace.is_contiguous()):
-            _refuse("workspace", workspace, "any type", "(*,)")
+        elif not (workspace.get_device() == self._device and workspace.is_contiguous()):
+            _refuse("workspace", workspace, "any type", "(*,)", self._device)
         return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def tree_decode(self, q_c, q_r, c_pool, k_pool, page_size: int, block_table, seq_lens, out, lse=None, mask=None,
@@ -324,8 +327,8 @@ class Plan:
         [B,T,H] fp32 or None."""
         T, qc, qr, lens, drafts, words = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        o = _expect("out", out, self._elem, (self.B, T, self.H, self.d_c))
-        z = None if lse is None else _expect("lse", lse, self._f32, (self.B, T, self.H))
+        o = self._expect("out", out, self._elem, (self.B, T, self.H, self.d_c))
+        z = None if lse is None else self._expect("lse", lse, self._f32, (self.B, T, self.H))
         ws, size = self._workspace(workspace, T, stream)
         st = self._lib.lca_tree_decode(self._h, qc, qr, T, *cache, lens, drafts, words, o, z, ws, size,
                                        self._call_stream(stream))
@@ -338,9 +341,9 @@ class Plan:
         these queries (lse from tree_decode; +inf leaves a row out).  prev may be scores, None stands for zeros."""
         T, qc, qr, lens, drafts, words = self._draft_args(q_c, q_r, seq_lens, draft_lens, mask)
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        z = _expect("lse", lse, self._f32, (self.B, T, self.H))
-        s = _expect_rows("scores", scores, self._f32, self.B)
-        before = None if prev is None else _expect("prev", prev, self._f32, scores.shape)
+        z = self._expect("lse", lse, self._f32, (self.B, T, self.H))
+        s = self._expect_rows("scores", scores, self._f32, self.B)
+        before = None if prev is None else self._expect("prev", prev, self._f32, scores.shape)
         ws, size = self._workspace(workspace, T, stream)
         st = self._lib.lca_attn_mass(self._h, qc, qr, T, *cache, lens, drafts, words, z, before, decay, s,
                                      scores.shape[1], ws, size, self._call_stream(stream))
@@ -351,9 +354,9 @@ class Plan:
         """lca_evict_select: the rows to keep, kept [B, budget] int32 rising, kept_lens [B] int32, from scores
         [B, stride] fp32: the first n_sink, the last n_recent and the largest sums between."""
         B, i32 = self.B, self._i32
-        st = self._lib.lca_evict_select(self._h, _expect_rows("scores", scores, self._f32, B), scores.shape[1],
-                                        _expect("seq_lens", seq_lens, i32, (B,)), n_sink, n_recent, kept.shape[-1],
-                                        _expect_rows("kept", kept, i32, B), _expect("kept_lens", kept_lens, i32, (B,)),
+        st = self._lib.lca_evict_select(self._h, self._expect_rows("scores", scores, self._f32, B), scores.shape[1],
+                                        self._expect("seq_lens", seq_lens, i32, (B,)), n_sink, n_recent, kept.shape[-1],
+                                        self._expect_rows("kept", kept, i32, B), self._expect("kept_lens", kept_lens, i32, (B,)),
                                         self._call_stream(stream))
         if st:
             raise LcaError(st, "lca_evict_select")
@@ -364,10 +367,10 @@ class Plan:
         (with the sums, if given): an eviction's kept rows, or a committed path of drafted tokens."""
         B, i32 = self.B, self._i32
         cache = self._cache_args(c_pool, k_pool, page_size, block_table)
-        to = None if dst0 is None else _expect("dst0", dst0, i32, (B,))
-        s, stride = (None, 0) if scores is None else (_expect_rows("scores", scores, self._f32, B), scores.shape[1])
-        st = self._lib.lca_cache_compact(self._h, *cache, _expect_rows("src", src, i32, B), src.shape[1],
-                                         _expect("n_src", n_src, i32, (B,)), to, s, stride, self._call_stream(stream))
+        to = None if dst0 is None else self._expect("dst0", dst0, i32, (B,))
+        s, stride = (None, 0) if scores is None else (self._expect_rows("scores", scores, self._f32, B), scores.shape[1])
+        st = self._lib.lca_cache_compact(self._h, *cache, self._expect_rows("src", src, i32, B), src.shape[1],
+                                         self._expect("n_src", n_src, i32, (B,)), to, s, stride, self._call_stream(stream))
         if st:
             raise LcaError(st, "lca_cache_compact")
 

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
               ptx::tmem_st32(tmem + ((uint32_t)(32 * quarter) << 16) + kColA + 32 * c, v);
             }
             ptx::named_bar_sync(kBarAdd, 32 * kAddWarps);          // the slot is read
-            if (sid == 0) ptx::mbar_arrive(empty + f);
+            if (sid == 0 && live) ptx::mbar_arrive(empty + f);     // (not after an error: nothing is loaded any more)
           }
           ptx::tmem_wait_st();
           ptx::tc_fence_before();

@@ -315,6 +315,100 @@ def test_longer_contexts(H, T, lens, page):
     check_mass(x, x.mass(plan, lse, prev, 1.0), lse, prev, 1.0)
 
 
+@pytest.mark.parametrize("B,H,T,most", [(40, 16, 3, 300), (150, 16, 2, 140), (33, 128, 3, 200), (40, 128, 9, 150), (70, 8, 3, 400)])
+def test_many_sequences(B, H, T, most):
+    """More sequences than lanes of a warp; more row blocks than the schedule splits; some without drafted tokens."""
+    r = np.random.default_rng(B)
+    lens = [int(r.integers(0, most)) for _ in range(B)]
+    drafts = [int(r.integers(0, T + 1)) for _ in range(B)]
+    drafts[3] = T
+    x = Batch(H, T, lens, drafts, page=64, seed=B)
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    ok(plan)
+    prev = torch.rand(x.B, x.cap, device="cuda")
+    s = x.mass(plan, lse, prev, 0.5)
+    ok(plan)
+    some = [0, 1, 3, 31, 32, B - 1]                          # the definition in 64 bits for a few of them
+    y = x.tree()
+    for a in ("lens", "drafts", "c", "k"):
+        setattr(y, a, [getattr(y, a)[b] for b in some])
+    y.q_c, y.q_r, y.words, y.B = y.q_c[some], y.q_r[some], y.words[some], len(some)
+    z = Batch.__new__(Batch)
+    z.B, z.drafts, z.dtype, z.tree = len(some), y.drafts, "bf16", lambda: y
+    check_tree(z, out[some], lse[some], tc=True)
+    check_mass(z, s[some], lse[some], prev[some], 0.5)
+    simt = x.plan()                                          # and all of them against the other kernels
+    simt.set(kvc.OPT_FORCE_SIMT, 1)
+    o2, z2 = x.decode(simt)
+    assert float((out.float() - o2.float()).abs().max()) <= 0.05
+    assert torch.allclose(lse, z2, rtol=0, atol=2e-4)
+    s2 = x.mass(simt, lse, prev, 0.5)
+    assert torch.allclose(s, s2, rtol=2e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 7])
+@pytest.mark.parametrize("H,T", [(16, 1), (16, 2), (16, 4), (128, 2)])
+def test_few_ctas(H, T, ctas):
+    x = Batch(H, T, [700, 0, 300], page=64, seed=31)
+    plan = x.plan()
+    plan.set(kvc.OPT_NUM_CTAS, ctas)
+    out, lse = x.decode(plan)
+    ok(plan)
+    check_tree(x, out, lse, tc=True)
+    check_mass(x, x.mass(plan, lse, None, 1.0), lse, None, 1.0)
+
+
+def test_nothing_drafted_at_all():
+    for lens in ([0, 0], [300, 40]):
+        x = Batch(16, 2, lens, [0, 0], page=64, seed=32, extra=3)
+        plan = x.plan()
+        out, lse = x.decode(plan)
+        assert bool((out == -77.0).all()) and bool((lse == -77.0).all())
+        prev = torch.rand(x.B, x.cap, device="cuda")
+        check_mass(x, x.mass(plan, lse, prev, 0.5), lse, prev, 0.5)
+        ok(plan)
+
+
+@pytest.mark.parametrize("H,T", [(16, 1), (16, 2), (16, 4), (24, 4), (128, 2)])
+def test_a_wait_that_runs_out_is_reported(H, T):
+    """The load that every CTA's first wait is for is left out: the bounded waits end, the error is reported, and the
+    next call of the same plan is right."""
+    x = Batch(H, T, [700, 130], page=64, seed=33)
+    plan = x.plan()
+    good, z = x.decode(plan)
+    s = x.mass(plan, z, None, 1.0)
+    plan.set(kvc.OPT_WAIT_TIMEOUT_NS, 20_000_000)
+    plan.set(kvc.OPT_DEBUG_SKIP_LOAD, 1)
+    x.decode(plan)
+    assert plan.device_error() == kvc.LCA_ERR_DEVICE_TIMEOUT
+    x.mass(plan, z, None, 1.0)
+    assert plan.device_error() == kvc.LCA_ERR_DEVICE_TIMEOUT
+    plan.set(kvc.OPT_DEBUG_SKIP_LOAD, 0)
+    plan.set(kvc.OPT_WAIT_TIMEOUT_NS, 2_000_000_000)
+    out, lse = x.decode(plan)
+    assert torch.equal(out, good) and torch.equal(lse, z)
+    assert torch.equal(x.mass(plan, z, None, 1.0), s)
+    ok(plan)
+
+
+def test_three_dimensional_and_strided_caches():
+    """[B, capacity, d] caches are taken as they are; a strided one is refused rather than copied."""
+    x = Batch(16, 2, [50, 90], seed=34)
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    c, k = x.c.view(2, x.cap, 512), x.k.view(2, x.cap, 64)
+    got = torch.full_like(out, -77.0)
+    plan.tree_decode(x.q_c, x.q_r, c, k, x.cap, None, x.dlens, got, mask=x.mask, draft_lens=x.ddrafts)
+    assert torch.equal(got, out)
+    wide = torch.zeros(2, x.cap, 600, dtype=BF16, device="cuda")[..., :512]
+    with pytest.raises(kvc.LcaError):
+        plan.tree_decode(x.q_c, x.q_r, wide, k, x.cap, None, x.dlens, got)
+    with pytest.raises(kvc.LcaError):
+        plan.cache_compact(wide, k, x.cap, None, torch.zeros(2, 1, dtype=torch.int32, device="cuda"),
+                           torch.ones(2, dtype=torch.int32, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype,H", [("bf16", 16), ("f32", 4)])
 def test_bad_lengths_and_pages_are_reported(dtype, H):
     kw = dict(dtype=dtype, **(dict(d_c=64, d_r=16) if dtype == "f32" else {}))
