@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
   const int64_t u0 = c0 < G ? c0 * U / G : 0, u1 = c0 < G ? (c0 + 1) * U / G : 0;
   Step st0 = {0, 0, 0, 1, 1};
   if (u0 < u1) {
-    const TreeUnit x = tree_unit(lanes, seq, t.B, 1, u0);
+    const TreeUnit x = tree_unit<int64_t>(lanes, seq, t.B, 1, u0);
     const TreeWork w = work(lens_of(x.b));
     st0 = Step{x.b, x.t0, x.rb, w.tiles, w.rb};
   }

@@ -46,8 +46,11 @@ struct TreeUnit {
   int t0, t1;                         // tiles
 };
 
-// First tile of part `part` of `parts` over `tiles`.
-LCA_HD int tree_cut(int tiles, int part, int parts) { return (int)((int64_t)tiles * part / parts); }
+// First tile of part `part` of `parts` over `tiles`: the first parts have one more where it does not come out even.
+LCA_HD int tree_cut(int tiles, int part, int parts) {
+  const int each = tiles / parts, more = tiles - each * parts;
+  return each * part + (part < more ? part : more);
+}
 
 // Units for parts of at most S tiles.  Lanes: lane() of count(), sum(), scan() (inclusive), first() (the lowest
 // lane where true, -1: none), get() (a lane's value).
@@ -103,23 +106,23 @@ LCA_HD int64_t tree_cost(int k, int S, int most) {
   return S > most ? INT64_MAX : (int64_t)k * (S + kTreeUnitCost);
 }
 
-// Unit u.
-template <class Lanes, class Seq>
-LCA_HD TreeUnit tree_unit(const Lanes& w, const Seq& seq, int B, int S, int64_t u) {
-  int64_t base = 0;
+// Unit u.  I holds the number of units.
+template <class I, class Lanes, class Seq>
+LCA_HD TreeUnit tree_unit(const Lanes& w, const Seq& seq, int B, int S, I u) {
+  I base = 0;
   for (int b0 = 0; b0 < B; b0 += w.count()) {
     const int b = b0 + w.lane();
     TreeWork k = {0, 0};
     if (b < B) k = seq(b);
     const int parts = (k.tiles + S - 1) / S;
-    const int64_t incl = base + w.scan((int64_t)k.rb * parts);
+    const I incl = base + w.scan((I)k.rb * parts);
     const int at = w.first(incl > u);
     if (at >= 0) {
       TreeUnit r;
       r.b = b0 + at;
       const int rb = w.get(k.rb, at), tiles = w.get(k.tiles, at);
       r.parts = w.get(parts, at);
-      const int i = (int)(u - (w.get(incl, at) - (int64_t)rb * r.parts));
+      const int i = (int)(u - (w.get(incl, at) - (I)rb * r.parts));
       r.part = i / rb;
       r.rb = i - r.part * rb;
       r.t0 = tree_cut(tiles, r.part, r.parts);
@@ -140,10 +143,11 @@ struct WarpLanes {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
-  __device__ __forceinline__ int64_t scan(int64_t v) const {
+  template <class I>
+  __device__ __forceinline__ I scan(I v) const {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+      const I x = __shfl_up_sync(0xffffffffu, v, o);
       if (lane() >= o) v += x;
     }
     return v;

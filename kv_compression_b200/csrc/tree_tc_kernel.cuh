@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     int nk = 0, nq = 0, slot = 0, use = 0;     // K tiles, query blocks; next slot, and how often each was filled
     int sent = 0;                              // slots that were ever filled (for the last waits)
     bool ok = true, skip = p.debug_skip_load != 0;
-    for (int64_t u = blockIdx.x; ok; u += p.G) {
-      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
+      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
       if (un.b < 0) break;
       const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;
@@ -308,7 +308,22 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       __syncwarp();
       ++nq;
       for (int tile = un.t0; tile < un.t1 && ok; ++tile) {
-        if (tile + 1 < un.t1) rows_of(tile + 1, n0, n1);
+        if (tile + 1 < un.t1) {
+          rows_of(tile + 1, n0, n1);
+          // Where several row blocks read the tile, the first brings the next one into L2, or the wait for
+          // memory would hold up all of them (V2-Lite trees 166 -> 156 us); where there is one, the slots
+          // in flight cover that wait and the prefetches only add to the traffic (148 sequences 438 -> 455).
+          if (un.rb == 0 && l.d * t.H > N && ptx::elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              ptx::tma_prefetch_l2_2d(&p.tm_c, 64 * c, n0);
+              ptx::tma_prefetch_l2_2d(&p.tm_c, 64 * c, n1);
+            }
+            ptx::tma_prefetch_l2_2d(&p.tm_k, 0, n0);
+            ptx::tma_prefetch_l2_2d(&p.tm_k, 0, n1);
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           if (i == kKAt) {
@@ -385,8 +400,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       }
       return full + slot;
     };
-    for (int64_t u = blockIdx.x; ok; u += p.G) {
-      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
+      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
       if (un.b < 0) break;
       ok = warp_wait(q_full, nq & 1, wt, 0xC20);
       ++nq;
@@ -515,8 +530,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
         base = lanes.get(incl, 31);
       }
     }
-    for (int64_t u = blockIdx.x; ok; u += p.G) {
-      const TreeUnit un = tree_unit(lanes, seq, t.B, S, u);
+    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
+      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
       if (un.b < 0) break;
       const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;

@@ -22,7 +22,7 @@ struct One {
   int lane() const { return 0; }
   int count() const { return 1; }
   int64_t sum(int64_t v) const { return v; }
-  int64_t scan(int64_t v) const { return v; }
+  template <class I> I scan(I v) const { return v; }
   int first(bool p) const { return p ? 0 : -1; }
   int get(int v, int) const { return v; }
   int64_t get(int64_t v, int) const { return v; }
@@ -78,13 +78,13 @@ int main() {
     for (int b = 0; b < B; ++b) seen[b].assign((size_t)ws[b].rb * ws[b].tiles, 0);
     const int64_t units = tree_units(one, seq, B, S);
     for (int64_t u = 0; u < units; ++u) {
-      const TreeUnit x = tree_unit(one, seq, B, S, u);
+      const TreeUnit x = u % 2 ? tree_unit<int64_t>(one, seq, B, S, u) : tree_unit<int>(one, seq, B, S, (int)u);
       if (x.b < 0 || x.t0 >= x.t1 || x.t1 - x.t0 > S || x.rb >= ws[x.b].rb || x.part >= x.parts)
         return printf("unit %lld is none\n", (long long)u), 1;
       if (x.parts > 1 && u >= (int64_t)kTreeMaxWaves * G) return printf("a slot past the workspace\n"), 1;
       for (int t = x.t0; t < x.t1; ++t) ++seen[x.b][(size_t)x.rb * ws[x.b].tiles + t];
     }
-    if (tree_unit(one, seq, B, S, units).b != -1) return printf("a unit too many\n"), 1;
+    if (tree_unit<int64_t>(one, seq, B, S, units).b != -1) return printf("a unit too many\n"), 1;
     for (auto& v : seen)
       for (int c : v)
         if (c != 1) return printf("a tile in %d units\n", c), 1;
