@@ -27,7 +27,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr size_t kMaxSmem = 232448;
+constexpr size_t kMaxSmem = 232448 - 1024;     // dynamic, beside what the CUDA-core kernels have besides
 
 // ---------------------------------------------------------------- workspace
 // [a record for each sequence][(M, Z) of every slot row][O of every slot row], each part
@@ -45,8 +45,9 @@ int simt_rows(const lca_plan* p, int T) {
   return wide ? lca::kTreeWideRows : lca::kTreeSimtRows;
 }
 
-// Parts the CUDA-core kernel cuts each sequence into: about four CTAs per SM
-// over B and the row blocks; one part writes its output itself.
+// Parts the CUDA-core kernel cuts each sequence into: about four CTAs per SM (two are resident at once) over B and
+// the row blocks; one part writes its output itself.  Half as many parts, one wave, are 8% faster for sequences of
+// one length and 25% slower for lengths from n / 4 to n, whose longest then sets the time.
 int64_t simt_parts(const lca_plan* p, int T) {
   const int64_t units = (int64_t)p->B * ceil_div((int64_t)T * p->H, simt_rows(p, T));
   const int64_t most = std::min<int64_t>(lca::kTreeMaxParts, ceil_div(p->max_L, lca::kTreeSimtTile));

@@ -14,7 +14,7 @@
 // FMAs), then 4 dims x 2 to 32 rows of the sum of values (3 reads for 32 FMAs at
 // d_c = 256).  Bound by shared memory reads (80% of the FMA rate for the
 // products), and by what its phases leave idle: two or more blocks an SM overlap.
-// Measured (192 rows over 3 x 30334 tokens, bf16): 393 us, against 2134 us with 8-row blocks.
+// Measured (192 rows over 3 x 30334 tokens, bf16): 294 us, against 2134 us with 8-row blocks.
 // Tokens that a row does not see are left out of every sum (no 0 x value), so
 // whatever their rows hold is not felt.
 #pragma once
@@ -25,6 +25,7 @@ namespace lca {
 constexpr int kTreeSimtRows = 8;       // warps
 constexpr int kTreeSimtTile = 32;      // tokens: lanes
 constexpr int kTreeSimtThreads = 256;
+constexpr int kTreeWideRows = 32;
 constexpr int kTreeSimtMaxDims = 4;    // d_c <= 1024: dims of a thread
 
 __host__ __device__ inline size_t tree_simt_smem(int d_c, int d_r) {
@@ -33,22 +34,29 @@ __host__ __device__ inline size_t tree_simt_smem(int d_c, int d_r) {
   return sizeof(float) * (kTreeSimtRows * d + kTreeSimtTile * (d + 4) + kTreeSimtRows * kTreeSimtTile + kTreeSimtRows);
 }
 
-// Stage tokens [t0, t0 + 32) of sequence b (those below `end`; zeros behind).
+// Stage `count` rows of d_c and d_r elements as fp32 rows of d_c + d_r + 4; list[j] is the j-th row's number, -1: zeros.
+// Every thread has four 4-element loads under way at a time (a row a warp, one after another, left the memory
+// latency in the open: 331 us against 258 for 22 rows over 6 x 37905 tokens of 160 dims).
 template <typename T>
-__device__ __forceinline__ void tree_stage_tile(const TreeBatch& t, int b, int t0, int end, float* tile, int where) {
-  const int dq = (t.d_c + t.d_r) / 4, cq = t.d_c / 4, stride = t.d_c + t.d_r + 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j = warp; j < kTreeSimtTile; j += kTreeSimtThreads / 32) {
-    float* dst = tile + (size_t)j * stride;
-    if (t0 + j >= end) {
-      for (int i = lane; i < dq; i += 32) *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
-      continue;
+__device__ __forceinline__ void tree_stage_rows(const void* c, const void* k, int d_c, int d_r, int count, const int* list, float* dst) {
+  const int dq = (d_c + d_r) / 4, cq = d_c / 4, stride = d_c + d_r + 4, total = count * dq;
+  constexpr int kAtOnce = 4;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kAtOnce * kTreeSimtThreads) {
+    float4 v[kAtOnce];
+    int at[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kTreeSimtThreads, j = i / dq, e = i - j * dq;
+      at[u] = j * stride + 4 * e;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < total && list[j] >= 0) {
+        const int64_t r = list[j];
+        v[u] = e < cq ? load4(static_cast<const T*>(c) + r * d_c + 4 * e) : load4(static_cast<const T*>(k) + r * d_r + 4 * (e - cq));
+      }
     }
-    const int64_t row = tree_row(t, b, t0 + j, where);
-    const T* c = static_cast<const T*>(t.c) + row * t.d_c;
-    const T* k = static_cast<const T*>(t.k) + row * t.d_r;
-    for (int i = lane; i < dq; i += 32)
-      *reinterpret_cast<float4*>(dst + 4 * i) = i < cq ? load4(c + 4 * i) : load4(k + 4 * (i - cq));
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i0 + u * kTreeSimtThreads < total) *reinterpret_cast<float4*>(dst + at[u]) = v[u];
   }
 }
 
@@ -97,6 +105,7 @@ struct TreeSimtParams {
 template <typename T>
 __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const TreeSimtParams p) {
   extern __shared__ float tree_smem[];
+  __shared__ int list[kTreeSimtTile];
   const TreeBatch& t = p.t;
   const int b = blockIdx.z, rb = blockIdx.y, s = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,7 +136,9 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
     for (int w = 0; w < kTreeSimtRows; ++w) acc[k][w] = 0.f;
   for (int t0 = lo; t0 < hi; t0 += kTreeSimtTile) {
     __syncthreads();
-    tree_stage_tile<T>(t, b, t0, hi, tile, 0xB02);
+    if (threadIdx.x < kTreeSimtTile) list[threadIdx.x] = t0 + (int)threadIdx.x < hi ? (int)tree_row(t, b, t0 + threadIdx.x, 0xB02) : -1;
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTreeSimtTile, list, tile);
     __syncthreads();
     const int pos = t0 + lane;
     float x = -INFINITY;
@@ -206,29 +217,12 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
 }
 
 // ---------------------------------------------------------------- blocks of 32 rows
-constexpr int kTreeWideRows = 32;
-
 __host__ __device__ inline size_t tree_wide_smem(int d_c, int d_r, int tokens) {
   const size_t d = (size_t)d_c + d_r + 4;
   return sizeof(float) * ((kTreeWideRows + tokens) * d + (size_t)tokens * (kTreeWideRows + 4) + 2 * kTreeWideRows);
 }
 // Tokens of a tile: 64 where two blocks then fit an SM.
-__host__ __device__ inline int tree_wide_tokens(int d_c, int d_r) { return tree_wide_smem(d_c, d_r, 64) <= 113 * 1024 ? 64 : 32; }
-
-// Stage `count` rows of d_c and d_r elements as fp32 rows of d_c + d_r + 4; row(j) gives the j-th row's number or -1 (zeros).
-template <typename T, class Row>
-__device__ __forceinline__ void tree_stage_rows(const void* c, const void* k, int d_c, int d_r, int count, float* dst, Row row) {
-  const int dq = (d_c + d_r) / 4, cq = d_c / 4, stride = d_c + d_r + 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j = warp; j < count; j += kTreeSimtThreads / 32) {
-    const int64_t r = row(j);
-    float* to = dst + (size_t)j * stride;
-    const T* pc = static_cast<const T*>(c) + r * d_c;
-    const T* pk = static_cast<const T*>(k) + r * d_r;
-    for (int i = lane; i < dq; i += 32)
-      *reinterpret_cast<float4*>(to + 4 * i) = r < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : i < cq ? load4(pc + 4 * i) : load4(pk + 4 * (i - cq));
-  }
-}
+__host__ __device__ inline int tree_wide_tokens(int d_c, int d_r) { return tree_wide_smem(d_c, d_r, 64) <= 112 * 1024 ? 64 : 32; }
 
 // Products of query rows 2 ty, 2 ty + 1 with tokens tx, tx + 16, ...
 template <int J>
@@ -256,6 +250,7 @@ template <typename T, int kTokens, int kRpt>
 __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const TreeSimtParams p) {
   constexpr int J = kTokens / 16, kPs = kTreeWideRows + 4;
   extern __shared__ float tree_smem[];
+  __shared__ int list[kTokens];
   const TreeBatch& t = p.t;
   const int b = blockIdx.z, rb = blockIdx.y, s = blockIdx.x, tid = threadIdx.x;
   const int ty = tid >> 4, tx = tid & 15;
@@ -273,7 +268,9 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
   const int64_t rows = (int64_t)ln.d * t.H, r0 = (int64_t)rb * kTreeWideRows;
   if (r0 >= rows) return;
   const int64_t q0 = (int64_t)b * t.T * t.H + r0;
-  tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, q, [&](int j) { return r0 + j < rows ? q0 + j : (int64_t)-1; });
+  if (tid < kTreeWideRows) list[tid] = r0 + tid < rows ? (int)(q0 + tid) : -1;
+  __syncthreads();
+  tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, list, q);
   unsigned long long word[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) word[k] = r0 + 2 * ty + k < rows ? tree_word(t, b, (int)((r0 + 2 * ty + k) / t.H)) : 0ull;
@@ -289,7 +286,9 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
   for (int k = 0; k < kRpt; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int t0 = lo; t0 < hi; t0 += kTokens) {
     __syncthreads();
-    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, tile, [&](int j) { return t0 + j < hi ? tree_row(t, b, t0 + j, 0xB02) : (int64_t)-1; });
+    if (tid < kTokens) list[tid] = t0 + tid < hi ? (int)tree_row(t, b, t0 + tid, 0xB02) : -1;
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, list, tile);
     __syncthreads();
     float x[2][J];
     tree_products<J>(q, tile, d, ty, tx, x);
@@ -331,14 +330,35 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
       const int tokens = min(kTokens, hi - t0);
       const float* vp = tile + 4 * g;
       const float* wp = pw + rg * kRpt;
-      for (int j = 0; j < tokens; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(vp + (size_t)j * stride);
+      auto add = [&](int k, float e, const float4& v) {
+        acc[k].x = fmaf(e, v.x, acc[k].x); acc[k].y = fmaf(e, v.y, acc[k].y);
+        acc[k].z = fmaf(e, v.z, acc[k].z); acc[k].w = fmaf(e, v.w, acc[k].w);
+      };
+      if (!special) {
+#pragma unroll 2
+        for (int j = 0; j < kTokens; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(vp + (size_t)j * stride);
+          float e[kRpt];
+          if constexpr (kRpt == 2) {
+            const float2 u = *reinterpret_cast<const float2*>(wp + j * kPs);
+            e[0] = u.x; e[1] = u.y;
+          } else {
 #pragma unroll
-        for (int k = 0; k < kRpt; ++k) {
-          const float e = wp[j * kPs + k];
-          if (!special || !(e < 0.f)) {
-            acc[k].x = fmaf(e, v.x, acc[k].x); acc[k].y = fmaf(e, v.y, acc[k].y);
-            acc[k].z = fmaf(e, v.z, acc[k].z); acc[k].w = fmaf(e, v.w, acc[k].w);
+            for (int k = 0; k < kRpt; k += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(wp + j * kPs + k);
+              e[k] = u.x; e[k + 1] = u.y; e[k + 2] = u.z; e[k + 3] = u.w;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kRpt; ++k) add(k, e[k], v);
+        }
+      } else {
+        for (int j = 0; j < tokens; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(vp + (size_t)j * stride);
+#pragma unroll
+          for (int k = 0; k < kRpt; ++k) {
+            const float e = wp[j * kPs + k];
+            if (!(e < 0.f)) add(k, e, v);
           }
         }
       }
@@ -409,6 +429,7 @@ __device__ __forceinline__ void mass_store(const MassParams& p, int b, int pos, 
 template <typename T>
 __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_simt_kernel(const MassParams p) {
   extern __shared__ float tree_smem[];
+  __shared__ int list[kTreeSimtTile];
   const TreeBatch& t = p.t;
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -422,7 +443,9 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_simt_kernel(const M
   const int total = ln.n + ln.d;
   for (int64_t t0 = (int64_t)blockIdx.x * kTreeSimtTile; t0 < total; t0 += (int64_t)gridDim.x * kTreeSimtTile) {
     __syncthreads();
-    tree_stage_tile<T>(t, b, (int)t0, total, tile, 0xB04);
+    if (threadIdx.x < kTreeSimtTile) list[threadIdx.x] = t0 + threadIdx.x < total ? (int)tree_row(t, b, (int)t0 + threadIdx.x, 0xB04) : -1;
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTreeSimtTile, list, tile);
     const int pos = (int)t0 + lane;
     float sum = 0.f;
     for (int64_t r0 = 0; r0 < rows; r0 += kTreeSimtRows) {
@@ -451,6 +474,7 @@ template <typename T, int kTokens>
 __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_wide_kernel(const MassParams p) {
   constexpr int J = kTokens / 16;
   extern __shared__ float tree_smem[];
+  __shared__ int list[kTokens];
   const TreeBatch& t = p.t;
   const int b = blockIdx.y, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int d = t.d_c + t.d_r, stride = d + 4;
@@ -463,14 +487,18 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_mass_wide_kernel(const M
   const int total = ln.n + ln.d;
   for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < total; t0 += (int64_t)gridDim.x * kTokens) {
     __syncthreads();
-    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, tile, [&](int j) { return t0 + j < total ? tree_row(t, b, (int)t0 + j, 0xB04) : (int64_t)-1; });
+    if (tid < kTokens) list[tid] = t0 + tid < total ? (int)tree_row(t, b, (int)t0 + tid, 0xB04) : -1;
+    __syncthreads();
+    tree_stage_rows<T>(t.c, t.k, t.d_c, t.d_r, kTokens, list, tile);
     const bool special = t0 + kTokens > ln.n;
     float sum[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) sum[j] = 0.f;
     for (int64_t r0 = 0; r0 < rows; r0 += kTreeWideRows) {
       __syncthreads();
-      tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, q, [&](int j) { return r0 + j < rows ? q0 + r0 + j : (int64_t)-1; });
+      if (tid < kTreeWideRows) list[tid] = r0 + tid < rows ? (int)(q0 + r0 + tid) : -1;
+      __syncthreads();
+      tree_stage_rows<T>(p.q_c, p.q_r, t.d_c, t.d_r, kTreeWideRows, list, q);
       __syncthreads();
       float x[2][J];
       tree_products<J>(q, tile, d, ty, tx, x);
