@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
   uint32_t prefix = 0, have = 0;                                // bits of the last key found; their mask
   {
     // the run's keys, line by line; row j of it is thread j / each's e = j % each
-    const uint32_t magic = (uint32_t)(((1ull << 32) + each - 1) / each);   // j / each = j magic >> 32 for these j
+    const uint32_t magic = (uint32_t)(((1ull << 32) + each - 1) / each);   // j magic >> 32 is j / each, or one more
     constexpr int kUnroll = 16;
     for (int u0 = 0; u0 < each; u0 += kUnroll) {
       float v[kUnroll];
@@ -143,7 +143,11 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
         const int j = (u0 + u) * kSelectThreads + tid, i = r0 + j;
         if (u0 + u >= each || i >= r1) continue;
         const uint32_t k = select_key(v[u]);
-        const int c = each == 1 ? j : (int)__umulhi((uint32_t)j, magic), e = j - c * each;
+        int c = each == 1 ? j : (int)__umulhi((uint32_t)j, magic), e = j - c * each;
+        if (e < 0) {                                            // one more: only with more than 2048 rows a thread
+          --c;
+          e += each;
+        }
         if (e < kSelectKeep) keys[e * kSelectStride + c] = k;
         if (i >= lo && i < hi) atomicAdd(&hist[k >> 24], 1);
       }

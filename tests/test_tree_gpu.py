@@ -539,6 +539,24 @@ def test_select_matches_definition(lens, stride, sink, recent, budget, kind):
         assert np.all(got[b, len(want):] == -7)
 
 
+@pytest.mark.parametrize("n", [20_000_000, 40_000_000])
+def test_select_of_very_long_sequences(n):
+    """Runs of thousands of rows a thread, where a row's place among the threads is no longer one multiplication."""
+    sink, recent, budget = 7, 1000, 30_001
+    g = torch.Generator(device="cuda").manual_seed(n)
+    s = torch.randint(0, 1 << 22, (1, n), generator=g, device="cuda").float()      # about 10 rows of each sum
+    kept = Guarded((1, budget), torch.int32, -7, -123456789)
+    kl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = kvc.Plan(1, 1, 8, 8, "f32", n)
+    plan.evict_select(s, torch.tensor([n], dtype=torch.int32).cuda(), sink, recent, kept.t, kl)
+    ok(plan)
+    top = torch.sort(s[0, sink:n - recent], descending=True, stable=True).indices[:budget - sink - recent] + sink
+    place = torch.cat([torch.arange(sink, device="cuda"), torch.arange(n - recent, n, device="cuda")])
+    assert int(kl) == budget
+    assert torch.equal(kept.t[0].long(), torch.sort(torch.cat([top, place])).values)
+    kept.check()
+
+
 def test_select_bad_length():
     plan = _select_plan(3, 100)
     x = torch.rand(3, 100, device="cuda")
