@@ -535,8 +535,9 @@ lca_status lca_evict_select(lca_plan *plan, const float *scores, int64_t score_s
  *              bounds positions); NULL: none
  * No page may be listed twice among the rows that move or are moved to (pages
  * shared by sequences must lie below dst0).  An entry of src that breaks its bounds
- * or order, or whose page is out of range, is not moved, a sequence whose n_src or
- * dst0 is out of range is left alone; either raises LCA_ERR_DEVICE_INPUT.
+ * or order is not moved, nor is the row (its sum may be) of one whose page is out of
+ * range, a sequence whose n_src or dst0 is out of range is left alone; each raises
+ * LCA_ERR_DEVICE_INPUT.
  * Errors: LCA_ERR_INVALID_ARG (as above; src_stride outside 1 .. 2^31 - 1),
  * LCA_ERR_UNSUPPORTED, LCA_ERR_ALIGNMENT (pools 16 bytes, the rest 4),
  * LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.

@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
 // It is bound by memory latency and then bandwidth: a strip is as wide as
 // leaves about one block per SM (narrower ones cost DRAM and L2 efficiency, wider
 // ones leave SMs idle).  Rows at their place already (src[j] = dst0 + j, the
-// first ones, since src[j] - j never falls) are passed over.
+// first ones, since src[j] - j never falls) are passed over, and one block
+// checks that they are.
 struct CompactParams {
   TreeBatch t;                  // the cache; lengths and masks unused
   int elem;                     // bytes of an element
@@ -303,6 +304,9 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
     first += (hit - 1) * step + 1;
     span = min(step - 1, end - first);
   }
+  if (blockIdx.x == 0)          // (the probes took the order on trust)
+    for (int j = tid; j < first; j += kCompactThreads)
+      if (src[j] != d0 + j) input_error(t.err, 0xB21);
   if (first >= m) return;
   auto valid = [&](int j, int s, int before) {
     const bool ok = s >= d0 + j && s < t.cap && (j == 0 || s > before);

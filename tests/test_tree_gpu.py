@@ -655,6 +655,26 @@ def test_compact_bad_lists_are_reported_and_harmless():
     assert np.array_equal(_bits(x.c), before)
 
 
+@pytest.mark.parametrize("at,value", [(101, 100), (50, 60), (3, -1)])
+def test_compact_reports_a_bad_entry_among_rows_at_their_place(at, value):
+    x = Batch(1, 1, [300, 300], page=64, seed=43)
+    plan = x.plan()
+    src = np.tile(np.arange(200, dtype=np.int32), (2, 1))
+    src[:, 199] = 250
+    src[1, at] = value
+    c0 = _bits(x.c).copy()
+    plan.cache_compact(x.c, x.k, 64, x.dtable, torch.from_numpy(src).cuda(), torch.tensor([200, 200], dtype=torch.int32).cuda())
+    assert plan.device_error() == kvc.LCA_ERR_DEVICE_INPUT
+    want = c0.copy()
+    for b in range(2):
+        want[x.rows(b, 199)] = c0[x.rows(b, 250)]
+    if value == 60:                                          # a good entry by itself; those after it break the order
+        got = _bits(x.c)
+        assert np.array_equal(got[x.rows(0, np.arange(300))], want[x.rows(0, np.arange(300))])
+    else:
+        assert np.array_equal(_bits(x.c), want)
+
+
 def test_checked_build():
     """The range-checked debug build over the small cases: no check fails, the same bounds hold."""
     lib = kbuild.build_checked()
