@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
   const int total = ln.n + ln.d;
   int per = (total + p.n_split - 1) / p.n_split;
   per = (per + kTreeSimtTile - 1) / kTreeSimtTile * kTreeSimtTile;
-  const int lo = (int)min((int64_t)total, (int64_t)s * per), hi = min(total, lo + per);
+  const int lo = (int)min((int64_t)total, (int64_t)s * per), hi = (int)min((int64_t)total, (int64_t)lo + per);
   float M = -INFINITY, Z = 0.f;
   float acc[kTreeSimtMaxDims][kTreeSimtRows];
 #pragma unroll

@@ -303,6 +303,27 @@ def test_rising_and_falling_logits(force):
         check_tree(x, out, lse, tc=not force)
 
 
+def test_the_longest_sequence():
+    """2^31 - 4097 positions over a few pages that the table lists again and again: the drafted token, the last of
+    them, has a logit of 60 where the others have none above 1, so it has all but e^(22 + 1 - 60) of the weight.  Both
+    bounds are a unit of fp32 and that share."""
+    cap = 2 ** 31 - 1 - 4096
+    pages = -(-cap // 64)
+    c = torch.rand(16 * 64, 8, device="cuda") / 8
+    k = torch.zeros(16 * 64, 8, device="cuda")
+    table = (torch.arange(pages, dtype=torch.int32, device="cuda") % 15)[None].contiguous()
+    table[0, -1] = 15
+    last = 15 * 64 + (cap - 1) % 64
+    c[last] = 60.0 / 8
+    q_c, q_r = torch.ones(1, 1, 1, 8, device="cuda"), torch.zeros(1, 1, 1, 8, device="cuda")
+    out, lse = torch.empty(1, 1, 1, 8, device="cuda"), torch.empty(1, 1, 1, device="cuda")
+    plan = kvc.Plan(1, 1, 8, 8, "f32", cap)
+    plan.tree_decode(q_c, q_r, c, k, 64, table, torch.tensor([cap - 1], dtype=torch.int32).cuda(), out, lse)
+    ok(plan)
+    assert float((out - 7.5).abs().max()) <= 7.5 * (2.0 ** -22 + np.exp(-37.0))
+    assert abs(float(lse) - 60.0) <= 60 * 2.0 ** -22
+
+
 @pytest.mark.parametrize("H,T,lens,page", [(16, 8, [5000, 9000, 1200], 64), (128, 3, [4000, 2500], 128),
                                            (16, 1, [20000], 0), (32, 5, [3000] * 9, 64)])
 def test_longer_contexts(H, T, lens, page):
