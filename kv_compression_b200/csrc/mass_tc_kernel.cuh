@@ -433,12 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         const uint32_t gaps = (gap[4 * buf + col0 / 32] >> (col0 % 32)) & all;
         if (special || gaps != 0u) {
           // the rows of these that see this thread's token, and are there; the others' logits become -inf
+          // (rows of nodes from 64 on, in a last block that is not full, are gaps)
           uint32_t sees = ~gaps;
           if (special) {
             int node = (at.rb * N + col0) / t.H, left = t.H - (at.rb * N + col0 - node * t.H);
             for (int c = 0; c < W; ++node, left = t.H) {
               const int n = min(left, W - c);
-              if (!((vis >> node) & 1ull)) sees &= ~((n == 32 ? ~0u : (1u << n) - 1u) << c);
+              if (!((vis >> (node & 63)) & 1ull)) sees &= ~((n == 32 ? ~0u : (1u << n) - 1u) << c);
               c += n;
             }
           }
