@@ -279,10 +279,12 @@ class Plan:
         return t.data_ptr()
 
     def _cache_args(self, c_pool, k_pool, page_size: int, block_table):
-        """The cache arguments of the C calls, checked: pools [rows, d] (or [B, capacity, d]) and an int32
+        """The cache arguments of the C calls, checked: pools [rows, d] or [pages, page_size, d] and an int32
         block_table [B, max_pages], or None for a contiguous cache with page_size rows a sequence."""
         rows = c_pool.shape[0]
         if c_pool.dim() == 3:
+            if c_pool.shape[1] != page_size:
+                raise LcaError(LCA_ERR_INVALID_ARG, f"c_pool: {tuple(c_pool.shape)} for page_size {page_size}")
             rows *= c_pool.shape[1]
             for what, t, d in (("c_pool", c_pool, self.d_c), ("k_pool", k_pool, self.d_r)):
                 self._expect(what, t, self._elem, (*c_pool.shape[:2], d))

@@ -430,6 +430,16 @@ def test_three_dimensional_and_strided_caches():
                            torch.ones(2, dtype=torch.int32, device="cuda"))
 
 
+def test_three_dimensional_caches_have_to_fit_the_page_size():
+    x = Batch(16, 2, [50, 90], seed=35)
+    plan = x.plan()
+    out, _ = x.decode(plan)
+    c, k = x.c.view(2, x.cap, 512), x.k.view(2, x.cap, 64)
+    for page in (x.cap - 1, x.cap // 2):
+        with pytest.raises(kvc.LcaError):
+            plan.tree_decode(x.q_c, x.q_r, c, k, page, None, x.dlens, out, mask=x.mask)
+
+
 @pytest.mark.parametrize("dtype,H", [("bf16", 16), ("f32", 4)])
 def test_bad_lengths_and_pages_are_reported(dtype, H):
     kw = dict(dtype=dtype, **(dict(d_c=64, d_r=16) if dtype == "f32" else {}))
