@@ -246,18 +246,24 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
 // ---------------------------------------------------------------- moving rows
 // Row dst0 + j of a sequence becomes its row src[j], j = 0 .. m - 1, in place;
 // src rises strictly and src[j] >= dst0 + j.  A block moves one strip of columns
-// (2, 4 or 8 times 16 bytes) of one sequence, tile after tile of rows in order.
+// (2 or 8 times 16 bytes) of one sequence, tile after tile of rows in order.
 // No row is overwritten before it is read: the rows of a tile are in registers
 // of the whole block before any of them is written, later tiles read only rows
 // above all those written so far (src[j] >= dst0 + j), and strips do not meet.
 // For the same reason the next tile's reads may be under way while this tile is
 // written, so two tiles (16 reads of 16 bytes a thread) are in flight.
 //
-// It is bound by memory latency and then bandwidth: a strip is as wide as
-// leaves about one block per SM (narrower ones cost DRAM and L2 efficiency, wider
-// ones leave SMs idle).  Rows at their place already (src[j] = dst0 + j, the
-// first ones, since src[j] - j never falls) are passed over, and one block
-// checks that they are.
+// It is bound by memory latency with few sequences and comes to 4.8 TB/s, read
+// and written, with 64.  Wide strips suit DRAM and L2, but a block for each SM
+// comes first: narrow ones as long as an SM gets no second block (4 sequences,
+// 16384 of 32768 rows each: 49 us, 61 with wide ones; 8 sequences, 8192 rows: 57,
+// wide 41), and 512 threads instead of 256 as long as all wide ones are resident
+// too (8 sequences: 41 instead of 54; with 32 37 instead of 35).  Two divisions a
+// row, for its page and place in it, had cost 10%.  Rows from behind the destination
+// copied whole by a second kernel, once this one has done the others, did not pay
+// (48 -> 51 to 54 us).  Rows at their place already (src[j] = dst0 + j, the first
+// ones, since src[j] - j never falls) are passed over, and one block checks that
+// they are.
 struct CompactParams {
   TreeBatch t;                  // the cache; lengths and masks unused
   int elem;                     // bytes of an element
@@ -268,11 +274,19 @@ struct CompactParams {
   float* scores;                // [B][score_stride]; null: none
   int64_t score_stride;
   int strips_c, strips_k;       // blocks for a row of c, of k; one more for the scores
+  uint32_t page_mul;            // of compact_page
+  int page_shift;
 };
 
-constexpr int kCompactThreads = 256;
+// A position's page, pos / page_size for 0 <= pos < 2^31, with mul = floor(2^(31 + l) / page_size) + 1 (below 2^32)
+// and shift = l - 1, l = ceil(log2 page_size) >= 1: mul page_size / 2^(31 + l) is above 1 by at most
+// page_size / 2^(31 + l) <= 2^-31, so the product's error stays below 1 / page_size.
+__device__ __forceinline__ uint32_t compact_page(const CompactParams& p, uint32_t pos) {
+  return __umulhi(pos, p.page_mul) >> p.page_shift;
+}
+
 constexpr int kCompactUnroll = 8;
-constexpr int kCompactMaxStrip = 8, kCompactMinStrip = 2;
+constexpr int kCompactWide = 8, kCompactNarrow = 2;          // strips, in 16 bytes
 
 // A row of the list on its way from the list to the copy: its loads are issued a
 // tile apart, so that none is waited for when it is needed.
@@ -281,8 +295,8 @@ struct CompactRow {
   int page_from, page_to;       // table entries
 };
 
-template <int kStrip>
-__global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const CompactParams p) {
+template <int kStrip, int kThreads>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) lca_compact_kernel(const CompactParams p) {
   const TreeBatch& t = p.t;
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int m = p.n_src[b];
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
     span = min(step - 1, end - first);
   }
   if (blockIdx.x == 0)          // (the probes took the order on trust)
-    for (int j = tid; j < first; j += kCompactThreads)
+    for (int j = tid; j < first; j += kThreads)
       if (src[j] != d0 + j) input_error(t.err, 0xB21);
   if (first >= m) return;
   auto valid = [&](int j, int s, int before) {
@@ -316,12 +330,12 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
   int sx = blockIdx.x;
   if (sx >= p.strips_c + p.strips_k) {
     float* sc = p.scores + (int64_t)b * p.score_stride;
-    for (int j0 = first; j0 < m; j0 += kCompactThreads * kCompactUnroll) {
+    for (int j0 = first; j0 < m; j0 += kThreads * kCompactUnroll) {
       float v[kCompactUnroll];
       bool ok[kCompactUnroll];
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
-        const int j = j0 + u * kCompactThreads + tid;
+        const int j = j0 + u * kThreads + tid;
         const int s = j < m ? src[j] : 0;
         ok[u] = j < m && valid(j, s, j > 0 ? src[j - 1] : -1);
         v[u] = ok[u] ? sc[s] : 0.f;
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u)
-        if (ok[u]) sc[d0 + j0 + u * kCompactThreads + tid] = v[u];
+        if (ok[u]) sc[d0 + j0 + u * kThreads + tid] = v[u];
       __syncthreads();
     }
     return;
@@ -344,9 +358,10 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
     base = static_cast<uint8_t*>(const_cast<void*>(t.k));
     row_bytes = t.d_r * p.elem;
   }
-  constexpr int kStep = kCompactThreads / kStrip;               // rows a block reads at once
+  constexpr int kStep = kThreads / kStrip;                      // rows a block reads at once
   constexpr int kRows = kStep * kCompactUnroll;                 // of a tile
-  constexpr int kEach = kRows / kCompactThreads;                // rows a thread looks up
+  constexpr int kEach = kRows / kThreads;                       // rows a thread looks up
+  static_assert(kRows % kThreads == 0, "every row of a tile is looked up");
   __shared__ int from_s[2][kRows], to_s[2][kRows];              // pool rows of a tile; -1: the row is left alone
   const int x = tid % kStrip, y = tid / kStrip;
   const bool act = x < row_bytes / 16 - sx * kStrip;
@@ -354,37 +369,38 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
   const uint32_t ps = (uint32_t)t.page_size;
   const int32_t* table = t.table ? t.table + (int64_t)b * t.max_pages : nullptr;
   CompactRow r[kEach], nx[kEach];
-  auto list = [&](int j0, CompactRow (&q)[kEach]) {             // the list's entries of the tile at j0
+  auto list = [&](uint32_t j0, CompactRow (&q)[kEach]) {        // the list's entries of the tile at j0
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int j = j0 + k * kCompactThreads + tid;
-      q[k].s = j < m ? src[j] : -1;
-      q[k].before = j < m && j > 0 ? src[j - 1] : -1;
+      const uint32_t j = j0 + k * kThreads + tid;
+      q[k].s = j < (uint32_t)m ? src[j] : -1;
+      q[k].before = j < (uint32_t)m && j > 0 ? src[j - 1] : -1;
     }
   };
-  auto pages = [&](int j0, CompactRow (&q)[kEach]) {            // their pages' table entries
+  auto pages = [&](uint32_t j0, CompactRow (&q)[kEach]) {       // their pages' table entries
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int j = j0 + k * kCompactThreads + tid;
-      if (q[k].s >= 0 || j < m) q[k].s = valid(j, q[k].s, q[k].before) ? q[k].s : -1;
+      const uint32_t j = j0 + k * kThreads + tid;
+      if (j < (uint32_t)m) q[k].s = valid(j, q[k].s, q[k].before) ? q[k].s : -1;
       q[k].page_from = q[k].page_to = b;
       if (table && q[k].s >= 0) {
-        q[k].page_from = table[(uint32_t)q[k].s / ps];
-        q[k].page_to = table[(uint32_t)(d0 + j) / ps];
+        q[k].page_from = table[compact_page(p, q[k].s)];
+        q[k].page_to = table[compact_page(p, d0 + j)];
       }
     }
   };
-  auto rows = [&](int j0, const CompactRow (&q)[kEach], int buf) {   // and their pool rows
+  auto rows = [&](uint32_t j0, const CompactRow (&q)[kEach], int buf) {   // and their pool rows
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int i = k * kCompactThreads + tid, to = d0 + j0 + i;
+      const uint32_t i = k * kThreads + tid, to = d0 + j0 + i;
       int from = -1, dst = -1;
       if (q[k].s >= 0) {
         if (table && (q[k].page_from < 0 || q[k].page_from >= t.num_pages || q[k].page_to < 0 || q[k].page_to >= t.num_pages)) {
           input_error(t.err, 0xB22);
         } else {
-          from = (int)(q[k].page_from * t.page_size + (uint32_t)q[k].s % ps);
-          dst = (int)(q[k].page_to * t.page_size + (uint32_t)to % ps);
+          // page' page_size + pos mod page_size
+          from = (int)((q[k].page_from - (table ? compact_page(p, q[k].s) : 0u)) * ps + q[k].s);
+          dst = (int)((q[k].page_to - (table ? compact_page(p, to) : 0u)) * ps + to);
         }
       }
       from_s[buf][i] = from;
@@ -401,18 +417,19 @@ __global__ void __launch_bounds__(kCompactThreads, 2) lca_compact_kernel(const C
       if (g[u] >= 0) d[u] = *reinterpret_cast<const uint4*>(base + (int64_t)from_s[buf][i] * row_bytes);
     }
   };
-  list(first, r);
-  list(first + kRows, nx);
-  pages(first, r);
-  rows(first, r, 0);
-  pages(first + kRows, nx);
+  const uint32_t j1 = first;
+  list(j1, r);
+  list(j1 + kRows, nx);
+  pages(j1, r);
+  rows(j1, r, 0);
+  pages(j1 + kRows, nx);
 #pragma unroll
   for (int k = 0; k < kEach; ++k) r[k] = nx[k];                 // r: the next tile, its pages under way
-  list(first + 2 * kRows, nx);                                  // nx: the one after it, its list under way
+  list(j1 + 2 * kRows, nx);                                     // nx: the one after it, its list under way
   __syncthreads();
   read(0, v, to);
   int buf = 0;
-  for (int j0 = first; j0 < m; j0 += kRows) {
+  for (uint32_t j0 = first; j0 < (uint32_t)m; j0 += kRows) {
     buf ^= 1;
     rows(j0 + kRows, r, buf);
 #pragma unroll

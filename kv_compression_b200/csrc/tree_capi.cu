@@ -458,17 +458,25 @@ lca_status lca_cache_compact(lca_plan* p, void* c_pool, void* k_pool, int64_t nu
   cp.dst0 = dst0;
   cp.scores = scores;
   cp.score_stride = score_stride;
-  // the widest strip that still makes blocks for three quarters of the SMs
-  const int64_t cols = (int64_t)(p->d_c + p->d_r) * cp.elem / 16;
-  int strip = lca::kCompactMaxStrip;
-  while (strip > lca::kCompactMinStrip && p->B * cols / strip < p->num_sms * 3 / 4) strip /= 2;
-  cp.strips_c = (int)ceil_div((int64_t)p->d_c * cp.elem / 16, strip);
-  cp.strips_k = (int)ceil_div((int64_t)p->d_r * cp.elem / 16, strip);
+  int l = 1;
+  while (l < 31 && (1LL << l) < page_size) ++l;
+  cp.page_mul = (uint32_t)((uint64_t(1) << (31 + l)) / (uint64_t)page_size + 1);
+  cp.page_shift = l - 1;
+  // Narrow strips while that makes no second block for an SM; wide ones, in blocks of 512 threads, while all of
+  // those are resident; else of 256.
+  const int64_t row_c = (int64_t)p->d_c * cp.elem / 16, row_k = (int64_t)p->d_r * cp.elem / 16;     // in 16 bytes
+  auto strips = [&](int strip) {
+    cp.strips_c = (int)ceil_div(row_c, strip);
+    cp.strips_k = (int)ceil_div(row_k, strip);
+    return (int64_t)(cp.strips_c + cp.strips_k + (scores ? 1 : 0)) * p->B <= p->num_sms;
+  };
+  const bool narrow = strips(lca::kCompactNarrow);
+  const bool few = narrow || strips(lca::kCompactWide);
   const dim3 grid((unsigned)(cp.strips_c + cp.strips_k + (scores ? 1 : 0)), (unsigned)p->B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (strip == 8) lca::lca_compact_kernel<8><<<grid, lca::kCompactThreads, 0, s>>>(cp);
-  else if (strip == 4) lca::lca_compact_kernel<4><<<grid, lca::kCompactThreads, 0, s>>>(cp);
-  else lca::lca_compact_kernel<2><<<grid, lca::kCompactThreads, 0, s>>>(cp);
+  if (narrow) lca::lca_compact_kernel<lca::kCompactNarrow, 512><<<grid, 512, 0, s>>>(cp);
+  else if (few) lca::lca_compact_kernel<lca::kCompactWide, 512><<<grid, 512, 0, s>>>(cp);
+  else lca::lca_compact_kernel<lca::kCompactWide, 256><<<grid, 256, 0, s>>>(cp);
   return launched();
 }
 

@@ -656,6 +656,62 @@ def test_compact_matches_definition(lens, page, keep, commit, dtype, d_c, d_r, s
         assert np.array_equal(sc.cpu().numpy(), want[2])
 
 
+@pytest.mark.parametrize("lens,page,first,keep,dtype,d_c,d_r", [
+    ([6000, 4000, 40, 5000], 64, [0, 100, 3, 0], [1100, 3899, 7, 0], "bf16", 512, 64),
+    ([6000, 1500], 0, [3500, 0], [1300, 1499], "bf16", 512, 64),          # all from behind; nearly all from within
+    ([9000], 192, [64], [2000], "bf16", 128, 32),
+    ([5000, 5000], 0, [0, 1], [1500, 1200], "f32", 64, 16),
+    ([4000], 64, [0], [2000], "f32", 1024, 256),
+    ([30000] * 3, 64, [4, 0, 9], [7500, 29000, 5], "bf16", 512, 64),
+])
+@pytest.mark.parametrize("again", [1, 3])
+def test_compact_of_long_lists(lens, page, first, keep, dtype, d_c, d_r, again):
+    """Lists of several tiles, from any first row, with rows from within and from behind the destination; also one
+    call behind another (the rows closed up, then taken out of each other's results)."""
+    x = Batch(1, 1, lens, page=page, dtype=dtype, d_c=d_c, d_r=d_r, seed=44)
+    r = np.random.default_rng(2)
+    sc = torch.rand(x.B, x.cap, device="cuda")
+    c, k, s = _bits(x.c), _bits(x.k), sc.cpu().numpy()
+    plan = x.plan()
+    for turn in range(again):
+        src = [np.sort(r.choice(np.arange(first[b], lens[b]), keep[b] // (turn + 1), replace=False)) for b in range(x.B)]
+        arr = np.full((x.B, max(len(a) for a in src) + 1), -5, np.int32)
+        for b, a in enumerate(src):
+            arr[b, :len(a)] = a
+        c, k, s = _compact_reference(x, src, first, c, k, s)
+        plan.cache_compact(x.c, x.k, x.page, x.dtable, torch.from_numpy(arr).cuda(),
+                           torch.tensor([len(a) for a in src], dtype=torch.int32).cuda(),
+                           dst0=torch.tensor(first, dtype=torch.int32).cuda(), scores=sc)
+    ok(plan)
+    assert np.array_equal(_bits(x.c), c) and np.array_equal(_bits(x.k), k) and np.array_equal(sc.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("kind", ["random", "falling", "far", "page"])
+def test_compact_long_bad_lists_stay_in_their_rows(kind):
+    """Whatever a list holds, only the rows it may name as destinations of its own sequence change."""
+    x = Batch(1, 1, [5000, 5000, 5000], page=64, seed=45)
+    m, r = 1200, np.random.default_rng(3)
+    src = np.tile(np.sort(r.choice(5000, m, replace=False)).astype(np.int32), (3, 1))
+    if kind == "random":
+        src[1] = r.integers(-2 ** 31, 2 ** 31 - 1, m)
+    elif kind == "falling":
+        src[1] = src[1, ::-1]
+    elif kind == "far":
+        src[1, 300:] = 10 ** 9
+    table = x.dtable.clone()
+    if kind == "page":
+        table[1, 40:] = 10 ** 6
+    c0 = _bits(x.c).copy()
+    want, _, _ = _compact_reference(x, [src[0], [], src[2]], [0, 0, 0], c0, _bits(x.k), None)
+    plan = x.plan()
+    plan.cache_compact(x.c, x.k, 64, table, torch.from_numpy(src).cuda(), torch.full((3,), m, dtype=torch.int32).cuda())
+    assert plan.device_error() == kvc.LCA_ERR_DEVICE_INPUT
+    got = _bits(x.c)
+    free = np.ones(len(c0), bool)
+    free[x.rows(1, np.arange(m))] = False
+    assert np.array_equal(got[free], want[free])
+
+
 def test_compact_bad_lists_are_reported_and_harmless():
     x = Batch(1, 1, [300, 300, 300], page=64, seed=13)
     plan = x.plan()
