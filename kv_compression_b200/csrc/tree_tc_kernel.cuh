@@ -37,7 +37,7 @@
 // with an infinity or NaN is zeroed too and makes the sums of the rows that see
 // it NaN.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs, the other 8 (N = 64: 16) do the
+// Roles: warp 0 finds the units and loads, warp 1 issues the MMAs, the other 8 (N = 64: 16) do the
 // softmax: a warp has 32 tokens (a TMEM lane quarter) and 8 or 16 of the rows.  Every wait
 // is bounded: when one runs out the CTA records it, lets its copies and MMAs
 // land, frees TMEM and exits.
@@ -62,6 +62,7 @@ constexpr int kMaxSlots = 5;
 // 2.4: 1.2e-6 before, 0.7e-6 after), in factors that are applied anyway.
 constexpr float kLogitScale = 1.f + 3.f / 8388608.f;
 constexpr float kLog2eS = (float)(1.4426950408889634 * (1.0 + 3.0 / 8388608.0));
+constexpr int kSeqs = 1024;                 // sequences whose work is kept in shared memory
 constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
 constexpr float kRaise = 8.f;
 constexpr int kErrTimeout = 1;
@@ -82,9 +83,11 @@ struct Layout {
   static constexpr int kOffRed = kOffWord + 8 * N;     // float [2][4][N], used in turn
   static constexpr int kOffM = kOffRed + 32 * N;       // float2 [N]: the rows' (M, Z)
   static constexpr int kOffBar = kOffM + 8 * N;
-  static constexpr int kBars = 2 * kMaxSlots + 8;
+  static constexpr int kBars = 2 * kMaxSlots + 10;
   static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S of k waves; nodes with a broken row;
-  static constexpr int kBytes = kOffMisc + 48;         // the event whose tile has to come back, the event it did
+  static constexpr int kOffUnit = kOffMisc + 48;       // the event whose tile has to come back, the event it did
+  static constexpr int kOffSeq = kOffUnit + 64;        // TreeUnit [2]: the softmax warps' units, 32 bytes each
+  static constexpr int kBytes = kOffSeq + 4 * kSeqs;   // u32 [kSeqs]: sequences' tiles and drafted tokens
   static constexpr int kAlloc = kBytes + 1024;         // slack for the 1 KB alignment
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
@@ -193,13 +196,15 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
   uint64_t *full = bars, *empty = bars + kMaxSlots, *k_full = bars + 2 * kMaxSlots, *k_empty = k_full + 1,
            *q_full = k_full + 2, *q_empty = k_full + 3, *drain = k_full + 4,
            *event = k_full + 5,       // for the softmax: S of a tile is there, a tile comes back, O is complete
-           *p_full = k_full + 6, *meet = k_full + 7;
+           *p_full = k_full + 6, *meet = k_full + 7,
+           *told = k_full + 8;        // [2]: a unit is written down for the softmax warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   int* s_least = reinterpret_cast<int*>(smem + L::kOffMisc + 8);       // [kTreeMaxWaves]
   unsigned long long* broken = reinterpret_cast<unsigned long long*>(smem + L::kOffMisc + 24);
   volatile int* too_high = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 32);
   volatile int* come_back = too_high + 1;
+  TreeUnit* units = reinterpret_cast<TreeUnit*>(smem + L::kOffUnit);
   const TreeBatch& t = p.t;
   const Wait wt = {abort_flag, t.err, p.timeout_ns};
   const WarpLanes lanes;
@@ -217,6 +222,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     ptx::mbar_init(p_full, kSoftmaxWarps);
     ptx::mbar_init(meet, kSoftmaxWarps);
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(told, 1);
+    ptx::mbar_init(told + 1, 1);
     *abort_flag = 0;
     *broken = 0ull;
     *too_high = *come_back = -1;
@@ -235,7 +242,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  // ---- the cut: one warp per number of waves.  Up to 32 sequences a lane keeps its own one's work.
+  // ---- the cut: one warp per number of waves.  Up to 32 sequences a lane keeps its own one's work; with more the
+  // first 1024 ones' is kept in shared memory, 25 bits of tiles and 7 of drafted tokens.
   const bool few = t.B <= 32;
   TreeWork own = {0, 0};
   TreeLens own_len = {0, 0, false};
@@ -247,8 +255,17 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     if (!few) return tree_lens(t, b);
     return TreeLens{__shfl_sync(0xffffffffu, own_len.n, b), __shfl_sync(0xffffffffu, own_len.d, b), false};
   };
+  uint32_t* kept = reinterpret_cast<uint32_t*>(smem + L::kOffSeq);
+  if (!few) {
+    for (int b = tid; b < min(t.B, kSeqs); b += L::kThreads) {
+      const TreeLens l = tree_lens(t, b);
+      kept[b] = (uint32_t)tree_work(l.n, l.d, t.H, N).tiles << 7 | (uint32_t)l.d;
+    }
+    __syncthreads();
+  }
   auto seq = [&](int b) {
     if (few) return own;                       // asked for b = lane only
+    if (b < kSeqs) return TreeWork{(int)((kept[b] & 127u) * (uint32_t)t.H + N - 1) / N, (int)(kept[b] >> 7)};
     const TreeLens l = tree_lens(t, b);
     return tree_work(l.n, l.d, t.H, N);
   };
@@ -282,9 +299,24 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     int nk = 0, nq = 0, slot = 0, use = 0;     // K tiles, query blocks; next slot, and how often each was filled
     int sent = 0;                              // slots that were ever filled (for the last waits)
     bool ok = true, skip = p.debug_skip_load != 0;
-    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
-      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
-      if (un.b < 0) break;
+    int nu = 0;
+    TreeCursor<int> at_unit;
+    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G, ++nu) {
+      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u, at_unit);
+      // Written down for the softmax warps, which have no registers for the search (V2 trees 442 -> 464 us with one).
+      // The entry was the one of two units ago, which they have read: the last unit's S is complete, and its first
+      // was issued after their P of the unit before it.
+      auto tell = [&] {
+        if (lane == 0) {
+          units[nu & 1] = un;
+          ptx::mbar_arrive(told + (nu & 1));
+        }
+        __syncwarp();
+      };
+      if (un.b < 0) {
+        if (nu < 2 || warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10)) tell();
+        break;
+      }
       const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;
       // a tile's two halves of 64 rows; a second half without tokens is loaded from the first half's rows, and
@@ -299,6 +331,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       const int qrow = (int)((int64_t)un.b * t.T * t.H + (int64_t)un.rb * N);
       if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10);
       if (!ok) break;
+      tell();
       if (ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(q_full, 9 * L::kQChunk);
 #pragma unroll
@@ -400,8 +433,9 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       }
       return full + slot;
     };
+    TreeCursor<int> at_unit;
     for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
-      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
+      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u, at_unit);
       if (un.b < 0) break;
       ok = warp_wait(q_full, nq & 1, wt, 0xC20);
       ++nq;
@@ -530,8 +564,10 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
         base = lanes.get(incl, 31);
       }
     }
-    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
-      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u);
+    int nu = 0;
+    for (int64_t u = blockIdx.x; ok; u += p.G, ++nu) {
+      if (!warp_wait(told + (nu & 1), (nu >> 1) & 1, wt, 0xC34)) break;
+      const TreeUnit un = units[nu & 1];
       if (un.b < 0) break;
       const TreeLens l = lens_of(un.b);
       const int total = l.n + l.d;

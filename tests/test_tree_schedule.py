@@ -103,3 +103,26 @@ def test_units_cover_every_tile_once(tmp_path):
     subprocess.run(["g++", "-O1", "-std=c++17", "-I" + os.path.join(ROOT, "kv_compression_b200", "csrc"), "-o", str(exe),
                     str(src)], check=True)
     assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "ok\n"
+
+
+def test_a_cursor_finds_the_same_units(tmp_path):
+    """The search that goes on from the last unit found, at the strides of a CTA's units."""
+    check = r"""
+    for (int64_t c = 0; c < G && c < units; ++c) {
+      TreeCursor<int> at;
+      for (int64_t u = c; u < units + G; u += G) {
+        const TreeUnit x = tree_unit<int>(one, seq, B, S, (int)u, at), y = tree_unit<int>(one, seq, B, S, (int)u);
+        if (x.b != y.b || (x.b >= 0 && (x.rb != y.rb || x.part != y.part || x.parts != y.parts || x.t0 != y.t0 || x.t1 != y.t1)))
+          return printf("unit %lld differs\n", (long long)u), 1;
+        if ((x.b < 0) != (u >= units)) return printf("unit %lld is there or not\n", (long long)u), 1;
+      }
+    }
+    for (auto& v : seen)"""
+    at = "\n    for (auto& v : seen)"
+    assert at in PROGRAM
+    src = tmp_path / "schedule.cpp"
+    src.write_text(PROGRAM.replace(at, check, 1).replace("round < 400", "round < 60"))
+    exe = tmp_path / "schedule"
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I" + os.path.join(ROOT, "kv_compression_b200", "csrc"), "-o", str(exe),
+                    str(src)], check=True)
+    assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "ok\n"
