@@ -108,7 +108,7 @@ LCA_HD int64_t tree_cost(int k, int S, int most) {
 
 // A place in the units' order: the batch of count() sequences looked at last, of which each lane keeps its own one.
 // A CTA's units follow one another, so each search goes on from the last (from the start every time, 4096
-// sequences took 1342 us).
+// sequences of 256 tokens took 1320 us for 600).
 template <class I>
 struct TreeCursor {
   int b0 = -1;                        // first sequence; -1: none looked at

@@ -62,7 +62,7 @@ constexpr int kMaxSlots = 5;
 // 2.4: 1.2e-6 before, 0.7e-6 after), in factors that are applied anyway.
 constexpr float kLogitScale = 1.f + 3.f / 8388608.f;
 constexpr float kLog2eS = (float)(1.4426950408889634 * (1.0 + 3.0 / 8388608.0));
-constexpr int kSeqs = 1024;                 // sequences whose work is kept in shared memory
+constexpr int kSeqs = 896;                  // sequences whose work is kept in shared memory
 constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
 constexpr float kRaise = 8.f;
 constexpr int kErrTimeout = 1;
@@ -80,13 +80,13 @@ struct Layout {
   static constexpr int kOffQ = kOffK + kChunk;
   static constexpr int kOffP = kAlias ? kOffK : kOffQ + 9 * kQChunk;
   static constexpr int kOffWord = kOffQ + 9 * kQChunk + (kAlias ? 0 : 128 * N * 2);   // mask words of the rows
-  static constexpr int kOffRed = kOffWord + 8 * N;     // float [2][4][N], used in turn
+  static constexpr int kOffRed = kOffWord + 16 * N;    // [2][N], used in turn; float [2][4][N], used in turn
   static constexpr int kOffM = kOffRed + 32 * N;       // float2 [N]: the rows' (M, Z)
   static constexpr int kOffBar = kOffM + 8 * N;
   static constexpr int kBars = 2 * kMaxSlots + 10;
   static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S of k waves; nodes with a broken row;
   static constexpr int kOffUnit = kOffMisc + 48;       // the event whose tile has to come back, the event it did
-  static constexpr int kOffSeq = kOffUnit + 64;        // TreeUnit [2]: the softmax warps' units, 32 bytes each
+  static constexpr int kOffSeq = kOffUnit + 64;        // Unit [2], used in turn
   static constexpr int kBytes = kOffSeq + 4 * kSeqs;   // u32 [kSeqs]: sequences' tiles and drafted tokens
   static constexpr int kAlloc = kBytes + 1024;         // slack for the 1 KB alignment
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
@@ -105,6 +105,12 @@ struct Params {
   float* lse;
   uint64_t timeout_ns;
   int debug_skip_load;
+};
+
+// A unit as the loading warp, which finds it, writes it down for the others.
+struct Unit {
+  TreeUnit un;
+  int n, d;                     // its sequence's lengths
 };
 
 struct Wait {
@@ -197,14 +203,15 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
            *q_full = k_full + 2, *q_empty = k_full + 3, *drain = k_full + 4,
            *event = k_full + 5,       // for the softmax: S of a tile is there, a tile comes back, O is complete
            *p_full = k_full + 6, *meet = k_full + 7,
-           *told = k_full + 8;        // [2]: a unit is written down for the softmax warps
+           *told = k_full + 8;        // [2]: a unit is written down
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   int* s_least = reinterpret_cast<int*>(smem + L::kOffMisc + 8);       // [kTreeMaxWaves]
   unsigned long long* broken = reinterpret_cast<unsigned long long*>(smem + L::kOffMisc + 24);
   volatile int* too_high = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 32);
   volatile int* come_back = too_high + 1;
-  TreeUnit* units = reinterpret_cast<TreeUnit*>(smem + L::kOffUnit);
+  Unit* units = reinterpret_cast<Unit*>(smem + L::kOffUnit);
+  static_assert(sizeof(Unit) == 32, "room for two");
   const TreeBatch& t = p.t;
   const Wait wt = {abort_flag, t.err, p.timeout_ns};
   const WarpLanes lanes;
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
   ptx::griddep_launch_dependents();
 
   // ---- the cut: one warp per number of waves.  Up to 32 sequences a lane keeps its own one's work; with more the
-  // first 1024 ones' is kept in shared memory, 25 bits of tiles and 7 of drafted tokens.
+  // first 896 ones' is kept in shared memory, 25 bits of tiles and 7 of drafted tokens.
   const bool few = t.B <= 32;
   TreeWork own = {0, 0};
   TreeLens own_len = {0, 0, false};
@@ -303,18 +310,19 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     TreeCursor<int> at_unit;
     for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G, ++nu) {
       const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u, at_unit);
-      // Written down for the softmax warps, which have no registers for the search (V2 trees 442 -> 464 us with one).
-      // The entry was the one of two units ago, which they have read: the last unit's S is complete, and its first
-      // was issued after their P of the unit before it.
-      auto tell = [&] {
+      // Written down for the other warps: the softmax warps have no registers for the search (V2 trees 442 -> 464 us
+      // with one), and in the MMA warp it held up the next S (3400 cycles with 740 sequences).  The entry was the
+      // one of two units ago, which all have read: the last unit's S is complete, and its first was issued after the
+      // P of the unit before it.
+      auto tell = [&](const TreeLens& of) {
         if (lane == 0) {
-          units[nu & 1] = un;
+          units[nu & 1] = Unit{un, of.n, of.d};
           ptx::mbar_arrive(told + (nu & 1));
         }
         __syncwarp();
       };
       if (un.b < 0) {
-        if (nu < 2 || warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10)) tell();
+        if (nu < 2 || warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10)) tell(TreeLens{0, 0, false});
         break;
       }
       const TreeLens l = lens_of(un.b);
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       const int qrow = (int)((int64_t)un.b * t.T * t.H + (int64_t)un.rb * N);
       if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1, wt, 0xC10);
       if (!ok) break;
-      tell();
+      tell(l);
       if (ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(q_full, 9 * L::kQChunk);
 #pragma unroll
@@ -433,9 +441,9 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       }
       return full + slot;
     };
-    TreeCursor<int> at_unit;
-    for (int64_t u = blockIdx.x; ok && u < INT32_MAX; u += p.G) {
-      const TreeUnit un = tree_unit<int>(lanes, seq, t.B, S, (int)u, at_unit);
+    while (ok) {
+      if (!warp_wait(told + (nq & 1), (nq >> 1) & 1, wt, 0xC21)) break;
+      const TreeUnit un = units[nq & 1].un;
       if (un.b < 0) break;
       ok = warp_wait(q_full, nq & 1, wt, 0xC20);
       ++nq;
@@ -531,12 +539,11 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     const int tok = 32 * quarter + lane;              // this thread's token of a tile
     const int sid = tid - 64;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + C * part;
-    unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord);
     float* reds = reinterpret_cast<float*>(smem + L::kOffRed);
     int red_turn = 0;
     float2* row_mz = reinterpret_cast<float2*>(smem + L::kOffM);
     uint8_t* pt = smem + L::kOffP + (C / 8) * part * 2048 + tok * 16;
-    int64_t np = 0;
+    int s0 = 0, ph = 0;         // slot of the tile's first load and the parity of its phase
     int ev = 0, met = 0;        // events seen; meetings of the softmax warps
     bool ok = true;
     // A barrier of the softmax warps whose wait is bounded: a warp that leaves on an error leaves none behind.
@@ -567,14 +574,14 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     int nu = 0;
     for (int64_t u = blockIdx.x; ok; u += p.G, ++nu) {
       if (!warp_wait(told + (nu & 1), (nu >> 1) & 1, wt, 0xC34)) break;
-      const TreeUnit un = units[nu & 1];
+      const TreeUnit un = units[nu & 1].un;
       if (un.b < 0) break;
-      const TreeLens l = lens_of(un.b);
+      const TreeLens l = TreeLens{units[nu & 1].n, units[nu & 1].d, false};
       const int total = l.n + l.d;
       const int rows = min(N, l.d * t.H - un.rb * N);
-      if (!meeting()) break;                           // the last unit's words and sums are read
+      unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + L::kOffWord) + N * (nu & 1);
       if (sid < N) words[sid] = sid < rows ? tree_word(t, un.b, (un.rb * N + sid) / t.H) : 0ull;
-      if (!meeting()) break;
+      if (!meeting()) break;                           // (and the last unit's sums are read)
       float nM[C], Z[C], x[C];    // -M in units of log2; x: the weights not yet in Z
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -591,7 +598,13 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
 #pragma unroll
           for (int c = 0; c < C; c += 2)
             ptx::f32x2_split(ptx::add_f32x2(ptx::f32x2(Z[c], Z[c + 1]), ptx::f32x2(x[c], x[c + 1])), Z[c], Z[c + 1]);
-          if (tile >= un.t0) np += 4;
+          if (tile >= un.t0) {
+            s0 += 4;
+            if (s0 >= kSlots) {
+              s0 -= kSlots;
+              ph ^= 1;
+            }
+          }
           ++tile;
         }
         ok = live;
@@ -603,17 +616,27 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
         uint32_t hurt = 0;                                     // rows that see this thread's broken token
         if (special) {
           // zero what is no token, and drafted rows that hold an infinity or NaN
-          for (int m = 0; m < 4; ++m)
-            ok = warp_wait(full + (np + m) % kSlots, (uint32_t)((np + m) / kSlots) & 1, wt, 0xC31) && ok;
+          auto slot_of = [&](int m) { return s0 + m < kSlots ? s0 + m : s0 + m - kSlots; };
+          auto phase_of = [&](int m) { return (uint32_t)(s0 + m < kSlots ? ph : ph ^ 1); };
+          bool there = true;                                   // S is complete, so the rows are; this makes them seen
+#pragma unroll
+          for (int m = 0; m < 4; ++m) there = ptx::mbar_test_wait(full + slot_of(m), phase_of(m)) && there;
+          if (!__all_sync(0xffffffffu, there))
+            for (int m = 0; m < 4; ++m) ok = warp_wait(full + slot_of(m), phase_of(m), wt, 0xC31) && ok;
+          uint8_t* chunk[2];                                   // 8 chunks of 128 bytes a row, 16 a lane
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ch = 4 * h + (lane >> 3);
+            chunk[h] = smem + slot_of(ch >> 1) * kSlot + (ch & 1) * kChunk + (lane & 7) * 16;
+          }
           for (int r = sw; r < kTreeTile; r += kSoftmaxWarps) {
             const int pos = pos0 + r;
             if (pos < l.n) continue;
             uint4* at[2];
             bool bad = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                      // 8 chunks of 128 bytes, 16 a lane
-              const int ch = 4 * h + (lane >> 3);
-              at[h] = reinterpret_cast<uint4*>(smem + ((np + (ch >> 1)) % kSlots) * kSlot + (ch & 1) * kChunk + r * 128) + (lane & 7);
+            for (int h = 0; h < 2; ++h) {
+              at[h] = reinterpret_cast<uint4*>(chunk[h] + r * 128);
               bad = bad || any_nonfinite(*at[h]);
             }
             bad = __any_sync(0xffffffffu, bad);
