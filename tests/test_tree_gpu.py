@@ -336,7 +336,8 @@ def test_longer_contexts(H, T, lens, page):
     check_mass(x, x.mass(plan, lse, prev, 1.0), lse, prev, 1.0)
 
 
-@pytest.mark.parametrize("B,H,T,most", [(40, 16, 3, 300), (150, 16, 2, 140), (33, 128, 3, 200), (40, 128, 9, 150), (70, 8, 3, 400)])
+@pytest.mark.parametrize("B,H,T,most", [(40, 16, 3, 300), (150, 16, 2, 140), (33, 128, 3, 200), (40, 128, 9, 150), (70, 8, 3, 400),
+                                        (1200, 16, 1, 150), (950, 16, 4, 140)])
 def test_many_sequences(B, H, T, most):
     """More sequences than lanes of a warp; more row blocks than the schedule splits; some without drafted tokens."""
     r = np.random.default_rng(B)
