@@ -18,7 +18,7 @@ SOURCES = {
                     "simt_kernel.cuh", "combine_kernel.cuh", "condense_kernel.cuh", "paged_kernel.cuh",
                     "gqa_kernel.cuh", "tmap.cuh"],
     "tree_capi.cu": ["checks.cuh", "device_input.cuh", "plan.cuh", "ptx.cuh", "tree_common.cuh",
-                     "tree_simt_kernel.cuh", "tree_schedule.cuh", "tree_tc_kernel.cuh", "mass_tc_kernel.cuh", "evict_kernel.cuh", "tmap.cuh"],
+                     "tree_simt_kernel.cuh", "tree_schedule.cuh", "tree_events.cuh", "tree_tc_kernel.cuh", "mass_tc_kernel.cuh", "evict_kernel.cuh", "tmap.cuh"],
 }
 HEADERS = sorted({h for hs in SOURCES.values() for h in hs})
 

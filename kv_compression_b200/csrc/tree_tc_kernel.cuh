@@ -47,6 +47,7 @@
 #include "checks.cuh"
 #include "ptx.cuh"
 #include "tree_common.cuh"
+#include "tree_events.cuh"
 #include "tree_schedule.cuh"
 
 namespace lca {
@@ -83,7 +84,7 @@ struct Layout {
   static constexpr int kOffRed = kOffWord + 16 * N;    // [2][N], used in turn; float [2][4][N], used in turn
   static constexpr int kOffM = kOffRed + 32 * N;       // float2 [N]: the rows' (M, Z)
   static constexpr int kOffBar = kOffM + 8 * N;
-  static constexpr int kBars = 2 * kMaxSlots + 10;
+  static constexpr int kBars = 2 * kMaxSlots + 11;
   static constexpr int kOffMisc = kOffBar + 8 * kBars; // TMEM address, abort, S of k waves; nodes with a broken row;
   static constexpr int kOffUnit = kOffMisc + 48;       // the event whose tile has to come back, the event it did
   static constexpr int kOffSeq = kOffUnit + 64;        // Unit [2], used in turn
@@ -201,9 +202,9 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t *full = bars, *empty = bars + kMaxSlots, *k_full = bars + 2 * kMaxSlots, *k_empty = k_full + 1,
            *q_full = k_full + 2, *q_empty = k_full + 3, *drain = k_full + 4,
-           *event = k_full + 5,       // for the softmax: S of a tile is there, a tile comes back, O is complete
-           *p_full = k_full + 6, *meet = k_full + 7,
-           *told = k_full + 8;        // [2]: a unit is written down
+           *event = k_full + 5,       // [2]: for the softmax: S of a tile is there, a tile comes back, O is complete
+           *p_full = k_full + 7, *meet = k_full + 8,
+           *told = k_full + 9;        // [2]: a unit is written down
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   int* s_least = reinterpret_cast<int*>(smem + L::kOffMisc + 8);       // [kTreeMaxWaves]
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
     ptx::mbar_init(k_empty, 1);
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
-    ptx::mbar_init(event, 1);
+    for (int i = 0; i < kTreeEventBars; ++i) ptx::mbar_init(event + i, 1);
     ptx::mbar_init(p_full, kSoftmaxWarps);
     ptx::mbar_init(meet, kSoftmaxWarps);
     ptx::mbar_init(drain, 1);
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
                                    d_q + (uint64_t)(((2 * m + ch) * L::kQChunk + 32 * k) >> 4), kIdS, (i | ch | k) != 0);
             }
             if (i == 4) {
-              ptx::mma_commit(event);
+              ptx::mma_commit(event + tree_event_bar(ev));
               if (tile + 1 == un.t1) ptx::mma_commit(q_empty);
             }
           }
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
           ++ev;
           if (lane == 0) {
             *come_back = ev;
-            ptx::mbar_arrive(event);
+            ptx::mbar_arrive(event + tree_event_bar(ev));
           }
           __syncwarp();
           ok = warp_wait(p_full, np++ & 1, wt, 0xC24);
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
             ptx::mma_commit(empty + slot);
           }
           if (L::kAlias) ptx::mma_commit(k_empty);
-          if (tile + 1 == un.t1) ptx::mma_commit(event);
+          if (tile + 1 == un.t1) ptx::mma_commit(event + tree_event_bar(ev));
         }
         __syncwarp();
         {
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       // one event after another: S of the next tile, the tile at hand once more, or the end
       bool special = false;
       for (int tile = un.t0 - 1;;) {
-        const bool live = warp_wait(event, ev & 1, wt, 0xC30);
+        const bool live = warp_wait(event + tree_event_bar(ev), tree_event_parity(ev), wt, 0xC30);
         ptx::tc_fence_after();
         const bool again = *come_back == ev;
         if (!again) {
