@@ -447,9 +447,9 @@ lca_status lca_decode_noalloc(int B, int H, int d_c, int d_r, lca_dtype dt, cons
  * once.
  */
 
-/* Bytes of workspace that lca_tree_decode and lca_attn_mass want for T = n_draft
- * (256-byte aligned, no initial contents, any use after the call); -1 for a NULL
- * plan or n_draft outside 1 .. 64. */
+/* Bytes of workspace that lca_tree_decode and lca_attn_mass want with up to n_draft
+ * nodes, T = 1 .. n_draft (256-byte aligned, no initial contents, any use after the
+ * call); -1 for a NULL plan or n_draft outside 1 .. 64. */
 int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
 
 /*
@@ -469,7 +469,7 @@ int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
  * lca_decode.
  * Errors: LCA_ERR_INVALID_ARG (NULL plan, q, pools, seq_lens, out or workspace;
  * n_draft outside 1 .. 64; sizes below 1; a paged page_size not a multiple of 64; a
- * contiguous num_pages < B; workspace_bytes below lca_tree_workspace),
+ * contiguous num_pages < B; workspace_bytes below what this n_draft wants),
  * LCA_ERR_UNSUPPORTED (2^31 rows or more, B T H >= 2^31, B > 65535, no kernel),
  * LCA_ERR_ALIGNMENT (q, pools, out: 16 bytes; workspace: 256; mask: 8; the rest: 4),
  * LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.

@@ -321,7 +321,11 @@ extern "C" {
 
 int64_t lca_tree_workspace(const lca_plan* p, int n_draft) {
   if (!p || n_draft < 1 || n_draft > lca::kTreeMaxDraft) return -1;
-  return (int64_t)workspace_of(p, n_draft).bytes;
+  // The CUDA-core kernels want less with more drafted tokens where those make row blocks enough: whoever asks for
+  // the largest tree has room for every smaller one.
+  size_t most = 0;
+  for (int T = 1; T <= n_draft; ++T) most = std::max(most, workspace_of(p, T).bytes);
+  return (int64_t)most;
 }
 
 lca_status lca_tree_decode(lca_plan* p, const void* q_c, const void* q_r, int n_draft, const void* c_pool,
