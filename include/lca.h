@@ -512,7 +512,8 @@ lca_status lca_attn_mass(lca_plan *plan, const void *q_c, const void *q_r, int n
  *   seq_lens   device int32 [B]: 0 <= n_b <= min(max_L, score_stride, 2^30)
  *   kept       device int32 [B][budget]: the kept rows of each sequence, rising;
  *              entries from kept_lens[b] on are left as they were
- *   kept_lens  device int32 [B]: min(n_b, budget); 0 where n_b is out of range
+ *   kept_lens  device int32 [B]: min(n_b, budget); 0 where n_b is out of range.  May be
+ *              seq_lens itself
  * Only B, max_L and the device of the plan count.  Errors: LCA_ERR_INVALID_ARG (NULL
  * pointers, score_stride < 1, budget < 1, n_sink or n_recent < 0 or their sum above
  * budget), LCA_ERR_ALIGNMENT (4 bytes), LCA_ERR_PLAN_MISMATCH, LCA_ERR_CUDA.

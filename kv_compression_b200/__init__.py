@@ -354,7 +354,8 @@ class Plan:
 
     def evict_select(self, scores, seq_lens, n_sink: int, n_recent: int, kept, kept_lens, stream=None) -> None:
         """lca_evict_select: the rows to keep, kept [B, budget] int32 rising, kept_lens [B] int32, from scores
-        [B, stride] fp32: the first n_sink, the last n_recent and the largest sums between."""
+        [B, stride] fp32: the first n_sink, the last n_recent and the largest sums between.  kept_lens may be
+        seq_lens."""
         B, i32 = self.B, self._i32
         st = self._lib.lca_evict_select(self._h, self._expect_rows("scores", scores, self._f32, B), scores.shape[1],
                                         self._expect("seq_lens", seq_lens, i32, (B,)), n_sink, n_recent, kept.shape[-1],

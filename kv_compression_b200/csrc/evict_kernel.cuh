@@ -36,7 +36,7 @@ struct SelectParams {
   int n_sink, n_recent;
   int budget;                   // entries a row of `kept` has
   int32_t* kept;                // [B][budget]
-  int32_t* kept_lens;           // [B]
+  int32_t* kept_lens;           // [B]; may be seq_lens
   int ctas;                     // of a cluster, which takes one sequence
   int* err;
 };
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
     }
     return;
   }
-  if (rank == 0 && tid == 0) p.kept_lens[b] = min(n, p.budget);
   if (n <= p.budget) {
+    if (rank == 0 && tid == 0) p.kept_lens[b] = n;              // (what others may still read there, in place)
     for (int i = rank * kSelectThreads + tid; i < n; i += ctas * kSelectThreads) kept[i] = i;
     return;
   }
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
       eq_before += eq;
     }
   ptx::cluster_sync();                                          // no CTA leaves while its counts may be read
+  if (rank == 0 && tid == 0) p.kept_lens[b] = p.budget;         // kept_lens may be seq_lens: every thread has read it
 }
 
 // ---------------------------------------------------------------- moving rows

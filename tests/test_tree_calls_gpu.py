@@ -34,3 +34,24 @@ def test_one_workspace_serves_every_smaller_tree(B, H, dtype, d_c, d_r):
     with pytest.raises(kvc.LcaError) as e:                   # still a refusal where it is too small
         x.decode(plan, ws=ws[:256])
     assert e.value.status == kvc.LCA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("lens,budget", [([5000, 300, 131072, 0, 40000, 512, 513, 9000], 512), ([900, 65, 64, 3], 64),
+                                         ([70000, -1, 99999999, 65000], 60000)])
+def test_kept_lens_in_place(lens, budget):
+    """The lengths become those that are kept in the tensor they come from; the same rows are kept."""
+    B, stride = len(lens), max(n for n in lens if n < 10 ** 7)
+    s = torch.rand(B, stride, generator=torch.Generator(device="cuda").manual_seed(budget), device="cuda")
+    plan = kvc.Plan(B, 1, 64, 16, "f32", stride)
+    want, kept = (torch.full((B, budget), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    lengths, kl = torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    bad = any(n < 0 or n > stride for n in lens)
+    plan.evict_select(s, lengths, 3, 16, want, kl)
+    assert plan.device_error() == (kvc.LCA_ERR_DEVICE_INPUT if bad else kvc.LCA_OK)
+    assert kl.tolist() == [min(n, budget) if 0 <= n <= stride else 0 for n in lens]
+    for _ in range(20):
+        n = lengths.clone()
+        kept.fill_(-7)
+        plan.evict_select(s, n, 3, 16, kept, n)
+        assert plan.device_error() == (kvc.LCA_ERR_DEVICE_INPUT if bad else kvc.LCA_OK)
+        assert torch.equal(n, kl) and torch.equal(kept, want)
