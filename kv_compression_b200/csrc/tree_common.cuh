@@ -95,6 +95,9 @@ constexpr float kTreeLn2 = 0.6931471805599453f;
 // 2^{m - top} for m <= top; 1 where they are equal, infinite ones among them.
 __device__ __forceinline__ float tree_scale(float m, float top) { return m == top ? 1.f : exp2f(m - top); }
 
+// What a row's logits are counted from: their maximum, 0 while all of them are -inf (weights of 0, not NaN).
+__device__ __forceinline__ float tree_origin(float top) { return top == -INFINITY ? 0.f : top; }
+
 struct TreeSplit {              // one per sequence, written by the main kernel
   int base;                     // slot of row block 0 of part 0
   int parts;                    // partials of each row; 0: none; 1: the main kernel wrote the output itself

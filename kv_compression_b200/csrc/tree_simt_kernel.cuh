@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(M, top);
     const bool live = r < rows && pos < hi && tree_sees(ln, word, pos);
-    const float e = live ? exp2f(x - top) : 0.f;
+    const float e = live ? exp2f(x - tree_origin(top)) : 0.f;
     const float f = tree_scale(M, top);
     M = top;
     float z = e;
@@ -310,10 +310,11 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
       top = fmaxf(M[k], top);
       const float f = tree_scale(M[k], top);
       M[k] = top;
+      const float origin = tree_origin(top);
       float z = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const float e = (seen >> j) & 1u ? exp2f(x[k][j] - top) : 0.f;
+        const float e = (seen >> j) & 1u ? exp2f(x[k][j] - origin) : 0.f;
         z += e;
         pw[(tx + 16 * j) * kPs + 2 * ty + k] = (seen >> j) & 1u ? e : -1.f;
       }

@@ -10,7 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import kv_compression_b200 as kvc  # noqa: E402
-from test_tree_gpu import Batch, ok  # noqa: E402
+from test_tree_gpu import UP_BF16, Batch, ok  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,59 @@ def test_kept_lens_in_place(lens, budget):
         plan.evict_select(s, n, 3, 16, kept, n)
         assert plan.device_error() == (kvc.LCA_ERR_DEVICE_INPUT if bad else kvc.LCA_OK)
         assert torch.equal(n, kl) and torch.equal(kept, want)
+
+
+def _masked_by_keys(H, dtype, value, **kw):
+    """A batch whose tokens named here have a key that makes their logits value / 2: the first 200 of a sequence (a
+    whole tile), all that are cached, those in the middle and at the end; and the indexes of the others."""
+    x = Batch(H, 3, [300, 130, 700, 140], page=64, seed=51, dtype=dtype, **kw)
+    x.q_r[..., 0] = 0.5
+    cut = [np.arange(200), np.arange(130), np.arange(390, 700), np.array([0, 128, 139])]
+    rest = []
+    for b, m in enumerate(cut):
+        rows = torch.from_numpy(x.rows_of[b][m]).cuda()
+        x.k[rows, 0] = value
+        rest.append(np.setdiff1d(np.arange(x.lens[b] + 3), m))
+    return x, cut, rest
+
+
+def _without(x, rest):
+    """The definition over the other tokens alone."""
+    t = x.tree()
+    for b, r in enumerate(rest):
+        t.lens[b] = int((r < x.lens[b]).sum())
+        t.c[b], t.k[b] = t.c[b][r], t.k[b][r]
+    return t
+
+
+def _check_masked(x, cut, rest, plan, tc):
+    out, lse = x.decode(plan)
+    ok(plan)
+    t = _without(x, rest)
+    want, wz, eo, ez = t.attend(UP_BF16 if tc else 0.0, UP_BF16 if x.dtype == "bf16" else 2.0 ** -24)
+    got, gz = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    right = bool(np.all(np.abs(got - want) <= eo)), bool(np.all(np.abs(gz - wz) <= ez))
+    assert right == (True, True)
+    s = x.mass(plan, lse, None, 1.0).double().cpu().numpy()
+    ok(plan)
+    for b, (m, e) in enumerate(t.mass(gz, None, 1.0)):
+        assert np.all(s[b, cut[b]] == 0)
+        assert np.all(np.abs(s[b, rest[b]] - m) <= e)
+
+
+KINDS = [(16, "bf16", False), (128, "bf16", False), (16, "bf16", True), (1, "bf16", True), (4, "f32", False), (1, "f32", False)]
+
+
+@pytest.mark.parametrize("H,dtype,force", KINDS)
+def test_tokens_with_logits_of_minus_infinity(H, dtype, force):
+    kw = {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    x, cut, rest = _masked_by_keys(H, dtype, float("-inf"), **kw)
+    plan = x.plan()
+    plan.set(kvc.OPT_FORCE_SIMT, int(force))
+    _check_masked(x, cut, rest, plan, dtype == "bf16" and not force)
+    for b in range(x.B):                                     # every row so: as if nothing were seen
+        x.k[torch.from_numpy(x.rows_of[b]).cuda(), 0] = float("-inf")
+    out, lse = x.decode(plan)
+    ok(plan)
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    assert bool((x.mass(plan, lse, None, 1.0)[:, :133] == 0).all())
