@@ -456,7 +456,7 @@ int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
  * Attention of drafted tokens: for node i < d_b and head h, with x_t = q_c.c_t +
  * q_r.k_t over the cached tokens and the drafted ones that node i sees,
  *   lse = log sum_t e^{x_t},  out = sum_t e^{x_t - lse} c_t.
- * A logit of -inf is a weight of 0.  A node that sees nothing (n_b = 0 and an empty
+ * A logit of -inf (tcgen05 kernel: below -9e7) is a weight of 0.  A node that sees nothing (n_b = 0 and an empty
  * mask word), or nothing but such logits, gives out = 0, lse = -inf.
  * T = 1 is the decode step over a cache of n_b + 1 rows.
  *   out        device, plan dtype [B][T][H][d_c] (rounded once, from fp32)

@@ -64,7 +64,10 @@ constexpr int kMaxSlots = 5;
 constexpr float kLogitScale = 1.f + 3.f / 8388608.f;
 constexpr float kLog2eS = (float)(1.4426950408889634 * (1.0 + 3.0 / 8388608.0));
 constexpr int kSeqs = 896;                  // sequences whose work is kept in shared memory
-constexpr float kEmpty = -1e30f;            // "no token yet": finite, so that differences of it are
+// M of a row with "no token yet", and its least: finite, so that differences of it are, and such that a weight
+// 2^{x log2 e - M}, whose M is the rounded product, stays in range where x is the maximum (off by up to 2^4 here).
+// With -1e30 rows whose first tile held nothing but logits of -5e14 gave NaN.
+constexpr float kEmpty = -134217728.f;
 constexpr float kRaise = 8.f;
 constexpr int kErrTimeout = 1;
 constexpr int kProbes = 64;

@@ -111,3 +111,25 @@ def test_tokens_with_logits_of_minus_infinity(H, dtype, force):
     ok(plan)
     assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
     assert bool((x.mass(plan, lse, None, 1.0)[:, :133] == 0).all())
+
+
+@pytest.mark.parametrize("value", [-3e38, -1e30, -1e20, -1e15, -1e10, -1e9, -1e6, -1e4])
+@pytest.mark.parametrize("H,dtype,force", KINDS)
+def test_tokens_masked_by_a_large_negative_logit(H, dtype, force, value):
+    """Half of `value` lies so far below the other logits (a few units) that its weight is 0 in fp32."""
+    kw = {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    x, cut, rest = _masked_by_keys(H, dtype, value, **kw)
+    plan = x.plan()
+    plan.set(kvc.OPT_FORCE_SIMT, int(force))
+    _check_masked(x, cut, rest, plan, dtype == "bf16" and not force)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_logits_that_the_tensor_cores_kernel_counts_as_minus_infinity(H):
+    x, _, _ = _masked_by_keys(H, "bf16", 0.0)
+    for b in range(x.B):
+        x.k[torch.from_numpy(x.rows_of[b]).cuda(), 0] = -1e10
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    ok(plan)
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
