@@ -462,11 +462,15 @@ int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
  *   out        device, plan dtype [B][T][H][d_c] (rounded once, from fp32)
  *   lse        device fp32 [B][T][H], natural logarithm; NULL: not wanted
  * Rows of nodes i >= d_b are left as they were; those of a sequence whose lengths
- * are out of range become NaN.  Where a drafted row holds an infinity or NaN, the
- * nodes that see it give NaN and the others are not touched by it.
+ * are out of range become NaN.
+ * A row that holds an infinity or NaN is felt by the nodes that see it and by no
+ * others, and by those as the formula has it: a logit of NaN or +inf makes out and
+ * lse NaN; one of -inf (an infinite key, say) is a weight of 0, which out feels in
+ * the dims alone where the row's C_KV is not finite (NaN there).  A drafted row
+ * whose C_KV is not finite may make all of the out and lse of those nodes NaN.
  * bf16 with (d_c, d_r) = (512, 64) runs a tcgen05 kernel (softmax weights rounded
- * to bf16 for their product with the values, everything else fp32); other plans the
- * CUDA-core kernel.  LCA_OPT_FORCE_SIMT and LCA_OPT_KERNEL 0 .. 2 choose as for
+ * to bf16 for their product with the values, everything else fp32; logits have to
+ * stay below 9e7); other plans the CUDA-core kernel.  LCA_OPT_FORCE_SIMT and LCA_OPT_KERNEL 0 .. 2 choose as for
  * lca_decode.
  * Errors: LCA_ERR_INVALID_ARG (NULL plan, q, pools, seq_lens, out or workspace;
  * n_draft outside 1 .. 64; sizes below 1; a paged page_size not a multiple of 64; a

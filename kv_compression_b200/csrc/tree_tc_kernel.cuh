@@ -34,8 +34,9 @@
 //
 // Tokens a row does not see get weight 0; because 0 x NaN is not 0, rows of
 // the tile that hold no token are zeroed in shared memory, and a drafted row
-// with an infinity or NaN is zeroed too and makes the sums of the rows that see
-// it NaN.
+// whose C holds an infinity or NaN is zeroed too and makes the sums of the rows
+// that see it NaN.  K is in the logits alone, which are selected and not
+// multiplied, so an infinite key needs no more.
 //
 // Roles: warp 0 finds the units and loads, warp 1 issues the MMAs, the other 8 (N = 64: 16) do the
 // softmax: a warp has 32 tokens (a TMEM lane quarter) and 8 or 16 of the rows.  Every wait

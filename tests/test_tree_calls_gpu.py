@@ -10,6 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import kv_compression_b200 as kvc  # noqa: E402
+import tree_reference as ref  # noqa: E402
 from test_tree_gpu import UP_BF16, Batch, ok  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +134,58 @@ def test_logits_that_the_tensor_cores_kernel_counts_as_minus_infinity(H):
     out, lse = x.decode(plan)
     ok(plan)
     assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+
+
+NOT_FINITE = [(which, v) for which in "ck" for v in (float("nan"), float("inf"), float("-inf"))]
+
+
+@pytest.mark.parametrize("where", ["drafted", "cached"])
+@pytest.mark.parametrize("lens", [[40] * 6, [126, 127, 300, 255, 128, 0]], ids=["one_tile", "tiles"])
+@pytest.mark.parametrize("H,dtype,force", KINDS)
+def test_rows_that_are_not_finite(H, dtype, force, lens, where):
+    """Every head of every node that sees such a row, by the logit that it makes: NaN and +inf make all NaN, -inf is a
+    weight of 0 and leaves NaN in the dims of C_KV that are not finite (a drafted row: may leave it everywhere)."""
+    kw = {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    lens = [max(n, 1) for n in lens] if where == "cached" else lens
+    x = Batch(H, 4, lens, page=64, seed=52, dtype=dtype, **kw)
+    x.set_words(ref.words_of(np.tile([-1, -1, 1, 0], (6, 1))))           # nodes 1 and 2 see node 1
+    at = [n + 1 if where == "drafted" else n // 2 for n in lens]
+    for b, (which, v) in enumerate(NOT_FINITE):
+        (x.c if which == "c" else x.k)[int(x.rows_of[b][at[b]]), 5] = v
+    feel = (1, 2) if where == "drafted" else (0, 1, 2, 3)
+    plan = x.plan()
+    plan.set(kvc.OPT_FORCE_SIMT, int(force))
+    out, lse = x.decode(plan)
+    ok(plan)
+    tc = dtype == "bf16" and not force
+    t = _without(x, [np.setdiff1d(np.arange(n + 4), a) if where == "cached" else np.arange(n + 4) for n, a in zip(lens, at)])
+    if where == "drafted":                                   # the definition without node 1's row
+        for b in range(6):
+            t.c[b][at[b]] = t.k[b][at[b]] = 0.0
+        t.words = t.words & ~np.uint64(2)
+    want, wz, eo, ez = t.attend(UP_BF16 if tc else 0.0, UP_BF16 if dtype == "bf16" else 2.0 ** -24)
+    got, gz = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    q = {"c": x.q_c[..., 5].double().cpu().numpy(), "k": x.q_r[..., 5].double().cpu().numpy()}
+    kinds = set()
+    for b, (which, v) in enumerate(NOT_FINITE):
+        for i in range(4):
+            for h in range(H):
+                o, z = got[b, i, h], gz[b, i, h]
+                near = np.abs(o - want[b, i, h]) <= eo[b, i, h] + 1e-30
+                same = z == wz[b, i, h] or abs(z - wz[b, i, h]) <= ez[b, i, h]
+                logit = v * q[which][b, i, h]
+                if i not in feel:
+                    kinds.add("other")
+                    assert near.all() and same, (b, i, h)
+                elif not logit < 0:
+                    kinds.add("all")
+                    assert np.isnan(o).all() and np.isnan(z), (b, i, h)
+                elif which == "k":
+                    kinds.add("key")
+                    assert near.all() and same, (b, i, h)
+                else:
+                    kinds.add("dim")
+                    may = where == "drafted"
+                    assert np.isnan(o[5]) and (near | (np.arange(x.d_c) == 5) | (may & np.isnan(o))).all(), (b, i, h)
+                    assert same or (may and np.isnan(z)), (b, i, h)
+    assert {"all", "key", "dim"} <= kinds
