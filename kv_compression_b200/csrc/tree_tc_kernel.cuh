@@ -61,7 +61,8 @@ constexpr int kMaxSlots = 5;
 // The tensor core cuts off where it adds.  Over a logit's 36 additions the partial sums lead up to the logit x on
 // average in equal steps, so what is cut off grows with x: measured -4.3e-7 x for random keys, -6.4e-7 x for keys
 // along the query, with half that beside it.  3 units of 2^-23 make up for most of the first (error of a logit of
-// 2.4: 1.2e-6 before, 0.7e-6 after), in factors that are applied anyway.
+// 2.4: 1.2e-6 before, 0.7e-6 after), in factors that are applied anyway.  A logit that is formed exactly pays for
+// it: 3.6e-7 x too much.
 constexpr float kLogitScale = 1.f + 3.f / 8388608.f;
 constexpr float kLog2eS = (float)(1.4426950408889634 * (1.0 + 3.0 / 8388608.0));
 constexpr int kSeqs = 896;                  // sequences whose work is kept in shared memory

@@ -189,3 +189,56 @@ def test_rows_that_are_not_finite(H, dtype, force, lens, where):
                     assert np.isnan(o[5]) and (near | (np.arange(x.d_c) == 5) | (may & np.isnan(o))).all(), (b, i, h)
                     assert same or (may and np.isnan(z)), (b, i, h)
     assert {"all", "key", "dim"} <= kinds
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_truncation_is_made_up_for_on_average(H):
+    """Full rows of random products: the tensor core's truncation, 4.3e-7 of a logit, less the factor's 3.6e-7.  The
+    bound of 2^-22 = 2.4e-7 of the logits at work (the weights' mean of them; 2^-21 beside it for the exponential, the
+    sums and the logarithm) holds neither without the factor nor with a wrong one.  The mean over the rows is compared:
+    the rest of a row's error is as often up as down."""
+    x = Batch(H, 1, [1000, 777, 1023, 900, 640, 810, 1001, 512], seed=53, scale=8.0)
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    ok(plan)
+    t = x.tree()
+    at_work, want = np.zeros((x.B, H)), np.zeros((x.B, H))
+    for b in range(x.B):
+        logits, _, _ = t.logits(b, 0)
+        m = logits.max(1, keepdims=True)
+        e = np.exp(logits - m)
+        want[b] = m[:, 0] + np.log(e.sum(1))
+        at_work[b] = (e * logits).sum(1) / e.sum(1)
+    assert at_work.mean() > 15
+    bound = 2.0 ** -22 * at_work.mean() + 2.0 ** -21
+    assert abs((lse[:, 0].double().cpu().numpy() - want).mean()) <= bound
+    z = torch.from_numpy(want).float().cuda()[:, None].contiguous()      # (rounded to nearest: as often up as down)
+    s = x.mass(plan, z, None, 1.0).double().cpu().numpy()
+    total = sum(s[b, :n + 1].sum() for b, n in enumerate(x.lens))
+    assert abs(total / (x.B * H) - 1) <= bound
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_logits_formed_exactly(H):
+    """One product a logit, of whole numbers: nothing is cut off, and lse is off by the factor's 3 2^-23 and at most six
+    roundings (the factor's constant, the product, M, ln 2, the sum, the last product), the weight by those in its
+    exponent."""
+    x = Batch(H, 1, [0] * 12, seed=54)
+    x.q_c.zero_()
+    x.q_r.zero_()
+    x.k.zero_()
+    value = torch.tensor([1, 2, 3, 5, 10, 20, 31, 60, -1, -7, -33, -60], dtype=torch.float32)
+    x.q_r[..., 7] = 1.0
+    for b in range(12):
+        x.k[int(x.rows_of[b][0]), 7] = float(value[b])
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    ok(plan)
+    want = value.double()[:, None].expand(12, H)
+    most = (3 * 2.0 ** -23 + 6 * 2.0 ** -24) * want.abs()
+    assert bool(((lse[:, 0].double().cpu() - want).abs() <= most).all())
+    for b in range(12):
+        assert bool((out[b] == x.c[int(x.rows_of[b][0])]).all())         # a weight of 1
+    s = x.mass(plan, want.float().cuda()[:, None].contiguous(), None, 1.0)[:, 0].double().cpu()
+    # H weights of 1 and what the exponent's error makes of them; 2^-20 for the exponential and the sum
+    assert bool(((s - H).abs() <= H * (most[:, 0] * 1.001 + 2.0 ** -20)).all())
