@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
           --c;
           e += each;
         }
+        if (!LCA_CHECK(p.err, e >= 0 && e < each && c >= 0 && c < kSelectThreads, 0xD70)) continue;
         if (e < kSelectKeep) keys[e * kSelectStride + c] = k;
         if (i >= lo && i < hi) atomicAdd(&hist[k >> 24], 1);
       }
@@ -236,7 +237,10 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
       bool sure, eq;
       judge(e, sure, eq);
       // of the rows with the last key the first `need` stay
-      if (sure || (eq && eq_before < need)) kept[sure_before + min(eq_before, need)] = first + e;
+      if (sure || (eq && eq_before < need)) {
+        const int at = sure_before + min(eq_before, need);
+        if (LCA_CHECK(p.err, at >= 0 && at < p.budget && first + e < n, 0xD71)) kept[at] = first + e;
+      }
       sure_before += sure;
       eq_before += eq;
     }
@@ -339,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) lca_compact_kernel(c
         const int j = j0 + u * kThreads + tid;
         const int s = j < m ? src[j] : 0;
         ok[u] = j < m && valid(j, s, j > 0 ? src[j - 1] : -1);
+        ok[u] = ok[u] && LCA_CHECK(t.err, s < p.score_stride && d0 + j < p.score_stride, 0xD72);
         v[u] = ok[u] ? sc[s] : 0.f;
       }
       __syncthreads();
@@ -402,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) lca_compact_kernel(c
           // page' page_size + pos mod page_size
           from = (int)((q[k].page_from - (table ? compact_page(p, q[k].s) : 0u)) * ps + q[k].s);
           dst = (int)((q[k].page_to - (table ? compact_page(p, to) : 0u)) * ps + to);
+          if (!LCA_CHECK(t.err, from >= 0 && from < t.num_pages * t.page_size && dst >= 0 && dst < t.num_pages * t.page_size, 0xD73))
+            from = dst = -1;
         }
       }
       from_s[buf][i] = from;

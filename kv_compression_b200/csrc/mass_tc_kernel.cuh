@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < kPer; ++k) {
             const int c = kPer * f + k;
-            if (c >= count) break;
+            if (c >= count || !LCA_CHECK(t.err, slot < kSlots && c < 9, 0xD60)) break;
             if (tiles) load_tile(dst + k * kChunk, c, full + slot);
             else load_q(dst + k * kChunk, c, full + slot);
           }
@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
         const int col0 = C * half + c0;
         const float* o = off + buf * N + col0;
         const uint32_t all = W == 32 ? ~0u : (1u << (W & 31)) - 1u;
+        if (!LCA_CHECK(t.err, col0 >= 0 && col0 + W <= N && buf < 2, 0xD62)) break;
         const uint32_t gaps = (gap[4 * buf + col0 / 32] >> (col0 % 32)) & all;
         if (special || gaps != 0u) {
           // the rows of these that see this thread's token, and are there; the others' logits become -inf
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) lca_mass_tc_kernel(const __grid_c
           const float sum = acc + part[tok];
           if (from_start && at.rb + 1 == at.rbs) {
             if (pos0 + tok < lat.n + lat.d) mass_store(p.m, at.b, pos0 + tok, lat.n, sum);
-          } else {
+          } else if (LCA_CHECK(t.err, (int)blockIdx.x < p.G, 0xD61)) {
             p.part[(2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0)) * kTreeTile + tok] = sum;
           }
         }
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kTreeTile) lca_mass_finish_kernel(const Finish
   for (int tile = blockIdx.x; tile < sp.tiles; tile += gridDim.x) {
     const int64_t u = sp.base + (int64_t)tile * sp.rb;
     const int64_t lo = ((u + 1) * G - 1) / U, hi = ((u + sp.rb) * G - 1) / U;   // the CTAs of its first and last step
-    if (lo == hi) continue;
+    if (lo == hi || !LCA_CHECK(p.m.t.err, lo >= 0 && hi < p.G, 0xD63)) continue;
     float sum = 0.f;
     for (int64_t c = lo; c <= hi; ++c) sum += p.part[(2 * c + (c * U / G < u ? 1 : 0)) * kTreeTile + tok];
     const int pos = tile * kTreeTile + tok;

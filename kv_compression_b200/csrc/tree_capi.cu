@@ -175,6 +175,7 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   sp.split = reinterpret_cast<lca::TreeSplit*>(ws);
   sp.part_mz = reinterpret_cast<float*>(ws + w.mz);
   sp.part_o = reinterpret_cast<float*>(ws + w.o);
+  sp.slot_rows = w.slot_rows;
   sp.out = out;
   sp.lse = lse;
   const int rows = simt_rows(p, t.T);
@@ -199,6 +200,7 @@ lca_status run_tree_simt(const lca_plan* p, const TreeBatch& t, const void* q_c,
   mp.part_o = sp.part_o;
   mp.part_mz = sp.part_mz;
   mp.split = sp.split;
+  mp.slot_rows = w.slot_rows;
   mp.rows_per_block = rows;
   mp.direct = sp.n_split == 1;
   mp.out = out;
@@ -243,6 +245,7 @@ lca_status run_tree_tc(const lca_plan* p, const TreeBatch& t, const void* q_c, c
   mp.part_o = tp.part_o;
   mp.part_mz = tp.part_mz;
   mp.split = tp.split;
+  mp.slot_rows = w.slot_rows;
   mp.rows_per_block = N;
   mp.direct = true;
   mp.out = out;

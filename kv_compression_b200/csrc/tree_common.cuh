@@ -12,6 +12,7 @@
 
 #include <cstdint>
 
+#include "checks.cuh"
 #include "device_input.cuh"
 
 namespace lca {
@@ -56,8 +57,10 @@ __device__ __forceinline__ unsigned long long tree_word(const TreeBatch& t, int 
 
 // The pool row of position `pos` of sequence b.
 __device__ __forceinline__ int64_t tree_row(const TreeBatch& t, int b, int pos, int where) {
-  if (!t.table) return (int64_t)b * t.page_size + pos;
-  return paged_row(t.table, t.max_pages, t.page_size, t.num_pages, b, pos, t.err, where);
+  if (!LCA_CHECK(t.err, pos >= 0 && pos < t.cap && b < t.B, 0xD50)) return 0;
+  const int64_t row = t.table ? paged_row(t.table, t.max_pages, t.page_size, t.num_pages, b, pos, t.err, where)
+                              : (int64_t)b * t.page_size + pos;
+  return LCA_CHECK(t.err, row >= 0 && row < t.num_pages * t.page_size, 0xD51) ? row : 0;
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -110,6 +113,7 @@ struct TreeMergeParams {
   const float* part_o;          // [slots][rows a block][d_c]
   const float* part_mz;         // [slots][rows a block][2]
   const TreeSplit* split;
+  int64_t slot_rows;            // rows of part_o and part_mz
   int rows_per_block;
   bool direct;                  // parts == 1 was written by the main kernel
   void* out;                    // [B][T][H][d_c] in the cache's type
@@ -158,6 +162,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads) lca_tree_merge_kernel(const
     const int rb = (int)(r / p.rows_per_block), col = (int)(r - (int64_t)rb * p.rows_per_block);
     const int64_t i0 = (int64_t)(sp.base + rb) * p.rows_per_block + col;     // the row in part 0's slot
     const int64_t step = (int64_t)sp.rb * p.rows_per_block;
+    if (!LCA_CHECK(p.t.err, sp.parts <= kTreeMaxParts && r < R && i0 + (sp.parts - 1) * step < p.slot_rows, 0xD52)) return;
     // M and Z over the parts: each thread its own, then the block's
     float M = -INFINITY, Z = 0.f;
     for (int s = tid; s < sp.parts; s += kTreeMergeThreads) {

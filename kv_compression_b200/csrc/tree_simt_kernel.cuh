@@ -96,6 +96,7 @@ struct TreeSimtParams {
   int n_split;                  // parts of a sequence (8 rows a slot); one part: the output is written here
   float* part_o;
   float* part_mz;
+  int64_t slot_rows;            // rows of both
   TreeSplit* split;
   void* out;
   float* lse;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_simt_kernel(const T
     return;
   }
   const int64_t i0 = (int64_t)(slot0 + s * (int)gridDim.y + rb) * kTreeSimtRows;
+  if (!LCA_CHECK(t.err, i0 + kTreeSimtRows <= p.slot_rows, 0xD53)) return;
 #pragma unroll
   for (int w = 0; w < kTreeSimtRows; ++w) {
     if (r0 + w >= rows) break;
@@ -372,13 +374,14 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
     for (int o = 8; o > 0; o >>= 1) Z[k] += __shfl_xor_sync(0xffffffffu, Z[k], o);
   }
   const int64_t i0 = (int64_t)(slot0 + s * (int)gridDim.y + rb) * kTreeWideRows;
+  const bool slot_ok = LCA_CHECK(t.err, p.n_split == 1 || i0 + kTreeWideRows <= p.slot_rows, 0xD54);
   __syncthreads();
   if (tx == 0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t r = r0 + 2 * ty + k;
       fac[2 * ty + k] = Z[k] == 0.f ? 0.f : 1.f / Z[k];
-      if (r >= rows) continue;
+      if (r >= rows || !slot_ok) continue;
       if (p.n_split > 1) {
         p.part_mz[2 * (i0 + 2 * ty + k)] = M[k];
         p.part_mz[2 * (i0 + 2 * ty + k) + 1] = Z[k];
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kTreeSimtThreads) lca_tree_wide_kernel(const T
     }
   }
   __syncthreads();
-  if (!act) return;
+  if (!act || !slot_ok) return;
 #pragma unroll
   for (int k = 0; k < kRpt; ++k) {
     const int r = rg * kRpt + k;
@@ -420,6 +423,7 @@ __device__ __forceinline__ float mass_offset(float lse) { return isinf(lse) ? -I
 
 // A position's new sum: cached tokens go on from what they had, drafted ones begin.
 __device__ __forceinline__ void mass_store(const MassParams& p, int b, int pos, int n, float add) {
+  if (!LCA_CHECK(p.t.err, pos >= 0 && pos < p.t.cap && pos < p.stride && b < p.t.B, 0xD55)) return;
   const int64_t i = (int64_t)b * p.stride + pos;
   float old = 0.f;
   if (pos < n && p.prev && p.decay != 0.f) old = p.decay * p.prev[i];

@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
           }
           const int m = i < kKAt ? i : i - 1;
           const int at = kSlots == 4 ? m : slot;
-          if (use > 0) ok = warp_wait(empty + at, (use - 1) & 1, wt, 0xC12);
+          if (!LCA_CHECK(t.err, at >= 0 && at < kSlots, 0xD42)) ok = false;
+          if (use > 0 && ok) ok = warp_wait(empty + at, (use - 1) & 1, wt, 0xC12);
           if (!ok) break;
           if (!skip && ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(full + at, kSlot);
@@ -643,6 +644,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               at[h] = reinterpret_cast<uint4*>(chunk[h] + r * 128);
+              if (!LCA_CHECK(t.err, chunk[h] >= smem && chunk[h] + r * 128 + 16 <= smem + kSlots * kSlot, 0xD43))
+                at[h] = reinterpret_cast<uint4*>(smem);
               bad = bad || any_nonfinite(*at[h]);
             }
             bad = __any_sync(0xffffffffu, bad);
@@ -752,7 +755,8 @@ __global__ void __launch_bounds__(Layout<N>::kThreads, 1) lca_tree_tc_kernel(con
       }
       if (!meeting()) break;
       // O^T: a thread has one dim and C rows of each block of 128 dims
-      const int mine = min(C, rows - C * part);                // rows of this thread
+      const bool out_ok = LCA_CHECK(t.err, row0 + rows <= (int64_t)t.B * t.T * t.H, 0xD44);
+      const int mine = out_ok ? min(C, rows - C * part) : 0;   // rows of this thread
       if (whole) {
         __nv_bfloat16* dst = p.out + (row0 + C * part) * kDC + tok;
         const float2* mz = row_mz + C * part;

@@ -11,6 +11,7 @@ if not torch.cuda.is_available():
 
 import kv_compression_b200 as kvc  # noqa: E402
 import tree_reference as ref  # noqa: E402
+from kv_compression_b200 import build as kbuild  # noqa: E402
 from test_tree_gpu import UP_BF16, Batch, ok  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -242,3 +243,52 @@ def test_logits_formed_exactly(H):
     s = x.mass(plan, want.float().cuda()[:, None].contiguous(), None, 1.0)[:, 0].double().cpu()
     # H weights of 1 and what the exponent's error makes of them; 2^-20 for the exponential and the sum
     assert bool(((s - H).abs() <= H * (most[:, 0] * 1.001 + 2.0 ** -20)).all())
+
+
+@pytest.fixture(scope="module")
+def checked():
+    return kbuild.build_checked()
+
+
+@pytest.mark.parametrize("H,T,lens,dtype,kw,opts", [
+    (16, 4, [700, 0, 300], "bf16", {}, {kvc.OPT_NUM_CTAS: 3}),                                  # several units a CTA
+    (16, 2, [100 + 3 * b for b in range(50)], "bf16", {}, {}),
+    (128, 9, [4000, 130], "bf16", {}, {}),
+    (128, 9, [400, 130, 77], "bf16", {}, {kvc.OPT_NUM_CTAS: 5}),
+    (16, 16, [9000], "bf16", {}, {}),
+    (16, 5, [900, 65], "bf16", {}, {kvc.OPT_FORCE_SIMT: 1}),
+    (3, 1, [900, 65], "bf16", {}, {kvc.OPT_FORCE_SIMT: 1}),
+    (2, 30, [900, 65], "f32", dict(d_c=64, d_r=16), {}),
+    (6, 12, [2000, 1], "bf16", dict(d_c=256, d_r=32), {}),
+])
+def test_checked_build_of_trees_and_weights(checked, H, T, lens, dtype, kw, opts):
+    """No check fires, and the same bits come out as from the ordinary build."""
+    x = Batch(H, T, lens, page=64, dtype=dtype, seed=55, **kw)
+    got = []
+    for lib in (None, checked):
+        plan = x.plan(lib_path=lib)
+        for k, v in opts.items():
+            plan.set(k, v)
+        out, lse = x.decode(plan)
+        s = x.mass(plan, lse, torch.ones(x.B, x.cap, device="cuda"), 0.5)
+        ok(plan)
+        got.append((out, lse, s))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens,budget", [([3000, 64, 65, 0, 2049], 64), ([131072, 40000], 16384), ([50000], 49999), ([500000], 70)])
+def test_checked_build_of_choice_and_compaction(checked, lens, budget):
+    x = Batch(1, 1, lens, page=64, seed=56, d_c=64, d_r=8)
+    s0 = torch.rand(x.B, x.cap, device="cuda")
+    n_src, got = torch.tensor(lens, dtype=torch.int32, device="cuda"), []
+    for lib in (None, checked):
+        plan = x.plan(lib_path=lib)
+        c, k, s, kl = x.c.clone(), x.k.clone(), s0.clone(), n_src.clone()
+        kept = torch.full((x.B, budget), -7, dtype=torch.int32, device="cuda")
+        plan.evict_select(s, kl, 4, 8, kept, kl)
+        plan.cache_compact(c, k, x.page, x.dtable, kept, kl, scores=s)
+        ok(plan)
+        got.append((kept, kl, c.view(torch.int16), k.view(torch.int16), s))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

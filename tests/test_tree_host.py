@@ -2,6 +2,8 @@
 any CUDA call, the mask helper, and pins of the 64-bit reference that the GPU
 tests compare with."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -92,3 +94,20 @@ def test_reference_select_by_hand():
     assert list(ref.select(s, 10, 0, 0, 9)) == [0, 1, 2, 3, 5, 6, 7, 8, 9]
     assert list(ref.select(s, 3, 1, 1, 4)) == [0, 1, 2]
     assert list(ref.select(s, 10, 2, 2, 4)) == [0, 1, 8, 9]
+
+
+def test_every_kernel_of_these_operators_checks_its_indexes():
+    """The range-checked build is of use where a kernel has checks: by itself, or in the lookups of pool rows and
+    sums that it calls."""
+    csrc = os.path.join(os.path.dirname(kbuild.__file__), "csrc")
+    found = []
+    for name in ("tree_common.cuh", "tree_simt_kernel.cuh", "tree_tc_kernel.cuh", "mass_tc_kernel.cuh", "evict_kernel.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for body in re.split(r"\b__global__\b", text)[1:]:
+            found.append(re.search(r"(lca_\w+_kernel)\(", body).group(1))
+            assert re.search(r"LCA_CHECK\(|tree_row\(|mass_store\(", body[:body.index("\n}\n")]), found[-1]
+        for helper in ("tree_row", "mass_store"):
+            if re.search(r"__forceinline__ \w+ " + helper + r"\(", text):
+                assert "LCA_CHECK(" in text.split(" " + helper + "(", 1)[1].split("\n}\n")[0], helper
+    assert len(found) == 10
