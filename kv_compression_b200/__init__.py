@@ -428,7 +428,8 @@ def slice_groups(L: int, g: int, w: int, pos0: int, n_tok: int) -> int:
 def tree_mask(parents):
     """The mask words of draft trees: parents int [B, T] (a torch tensor, on any device), parents[b, i] < i the
     parent of node i, -1 where it follows the cached tokens.  Returns int64 [B, T]: bit j of word i says that
-    node j is node i or one of its ancestors."""
+    node j is node i or one of its ancestors.  The parents are checked on the host: with a tensor on a GPU the call
+    waits for it, and cannot be captured in a graph (make the words before, from a tensor on the CPU say)."""
     import torch
     p = parents.to(torch.int64)
     B, T = p.shape

@@ -292,3 +292,23 @@ def test_checked_build_of_choice_and_compaction(checked, lens, budget):
         got.append((kept, kl, c.view(torch.int16), k.view(torch.int16), s))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_mask_words_from_parents_on_either_side():
+    """Made from parents on the CPU the words need no wait; a graph of the other calls takes them as they then are."""
+    x = Batch(16, 5, [200, 60], page=64, seed=57)
+    parents = [torch.tensor([[-1, 0, 0, 1, 3], [-1, -1, 1, 1, 0]]), torch.tensor([[-1, 0, 1, 2, 3], [-1, 0, 0, 2, -1]])]
+    plan, ws = x.plan(), x.plan().tree_workspace(5)
+    x.mask = kvc.tree_mask(parents[0]).cuda()
+    assert torch.equal(x.mask, kvc.tree_mask(parents[0].cuda()))
+    out, z = torch.zeros_like(x.q_c), torch.zeros(2, 5, 16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.tree_decode(x.q_c, x.q_r, x.c, x.k, x.page, x.dtable, x.dlens, out, z, mask=x.mask, workspace=ws)
+    for p in parents:
+        x.mask.copy_(kvc.tree_mask(p))
+        g.replay()
+        torch.cuda.synchronize()
+        want, wz = x.decode(plan)
+        assert torch.equal(out, want) and torch.equal(z, wz)
+    ok(plan)
