@@ -423,7 +423,11 @@ lca_status lca_evict_select(lca_plan* p, const float* scores, int64_t score_stri
   sp.kept = kept;
   sp.kept_lens = kept_lens;
   sp.err = p->err;
-  // One CTA for up to 4096 rows, twice as many for twice the rows, up to a cluster of 8.
+  // One CTA for up to 4096 rows, twice as many for twice the rows, up to a cluster of 8.  Measured with 1 / 2 / 4 / 8
+  // CTAs, 8 sequences, a quarter kept (us): 4096 rows 11.5 / 10.8 / 10.1 / 10.6, 8192 14.6 / 12.3 / 11.3 / 11.3, 16384
+  // 19.8 / 15.1 / 12.6 / 12.2, 32768 31 / 20 / 15.1 / 13.2, 131072 304 / 115 / 36 / 25.  The rule does not look at B:
+  // where all CTAs are not resident at once fewer are faster (32 x 32768: 37 with 8, 16 with 4; 128 x 8192: 23 with
+  // 2, 15 with 1).
   sp.ctas = 1;
   while (sp.ctas < lca::kSelectMaxCtas && sp.cap > 4096LL * sp.ctas) sp.ctas *= 2;
   if (p->B > INT32_MAX / lca::kSelectMaxCtas) return LCA_ERR_UNSUPPORTED;
