@@ -471,7 +471,7 @@ int64_t lca_tree_workspace(const lca_plan *plan, int n_draft);
  * bf16 with (d_c, d_r) = (512, 64) runs a tcgen05 kernel (softmax weights rounded
  * to bf16 for their product with the values, everything else fp32; logits have to
  * stay below 9e7); other plans the CUDA-core kernel.  The tensor core cuts off where
- * it adds, which costs a logit of 576 products about 4.3e-7 of itself; its logits are
+ * it adds, which costs a logit of 576 products 4e-7 to 6e-7 of itself; its logits are
  * therefore multiplied by 1 + 3 2^-23 (here and in lca_attn_mass), so that one which
  * it forms exactly (few products, small whole numbers) comes out 3.6e-7 of itself
  * too large: 2.1e-5 in lse, and in a weight's exponent, at a logit of 60.  LCA_OPT_FORCE_SIMT and LCA_OPT_KERNEL 0 .. 2 choose as for

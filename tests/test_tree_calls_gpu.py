@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
 import kv_compression_b200 as kvc  # noqa: E402
 import tree_reference as ref  # noqa: E402
 from kv_compression_b200 import build as kbuild  # noqa: E402
-from test_tree_gpu import UP_BF16, Batch, ok  # noqa: E402
+from test_tree_gpu import UP_BF16, Batch, check_mass, check_tree, ok  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -194,7 +194,7 @@ def test_rows_that_are_not_finite(H, dtype, force, lens, where):
 
 @pytest.mark.parametrize("H", [16, 128])
 def test_truncation_is_made_up_for_on_average(H):
-    """Full rows of random products: the tensor core's truncation, 4.3e-7 of a logit, less the factor's 3.6e-7.  The
+    """Full rows of random products: the tensor core's truncation, 4e-7 to 6e-7 of a logit, less the factor's 3.6e-7.  The
     bound of 2^-22 = 2.4e-7 of the logits at work (the weights' mean of them; 2^-21 beside it for the exponential, the
     sums and the logarithm) holds neither without the factor nor with a wrong one.  The mean over the rows is compared:
     the rest of a row's error is as often up as down."""
@@ -312,3 +312,144 @@ def test_mask_words_from_parents_on_either_side():
         want, wz = x.decode(plan)
         assert torch.equal(out, want) and torch.equal(z, wz)
     ok(plan)
+
+
+@pytest.mark.parametrize("H,dtype,page", [(16, "bf16", 64), (128, "bf16", 0), (4, "f32", 64)])
+def test_a_whole_step_captured(H, dtype, page):
+    """Copies, another stream's work, attention, weights, commit, choice and compaction in one graph, behind one
+    another; replayed with other contents it does what the calls do one by one."""
+    T, kw = 4, {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    x = Batch(H, T, [300, 5000, 129], page=page, seed=58, dtype=dtype, extra=20, **kw)
+    x.c.nan_to_num_(0.0)
+    x.k.nan_to_num_(0.0)
+    plan, budget = x.plan(), 128
+    host = [x.q_c.cpu().pin_memory(), (x.q_c * -0.5).cpu().pin_memory()]
+    src = torch.stack([torch.tensor([n + 1, n + 3]) for n in x.lens]).int().cuda()
+    two = torch.full((3,), 2, dtype=torch.int32, device="cuda")
+
+    class State:
+        def __init__(self):
+            self.c, self.k, self.q = x.c.clone(), x.k.clone(), torch.zeros_like(x.q_c)
+            self.lens, self.scores = x.dlens.clone(), torch.rand(3, x.cap, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+            self.out, self.lse = torch.zeros_like(x.q_c), torch.zeros(3, T, H, device="cuda")
+            self.kept = torch.zeros(3, budget, dtype=torch.int32, device="cuda")
+            self.ws = plan.tree_workspace(T)
+            self.side = torch.cuda.Stream()
+
+        def reset(self):
+            for a, b in ((self.c, x.c), (self.k, x.k), (self.lens, x.dlens)):
+                a.copy_(b)
+            self.scores.copy_(State().scores)
+
+        def step(self, q):
+            here = torch.cuda.current_stream()
+            self.side.wait_stream(here)
+            with torch.cuda.stream(self.side):               # something else that the attention waits for
+                self.scores.mul_(0.5)
+            self.q.copy_(q, non_blocking=True)
+            here.wait_stream(self.side)
+            plan.tree_decode(self.q, x.q_r, self.c, self.k, x.page, x.dtable, self.lens, self.out, self.lse, mask=x.mask, workspace=self.ws)
+            self.side.wait_stream(here)
+            with torch.cuda.stream(self.side):
+                self.scores.add_(0.25)
+            here.wait_stream(self.side)
+            plan.attn_mass(self.q, x.q_r, self.c, self.k, x.page, x.dtable, self.lens, self.lse, self.scores, prev=self.scores,
+                           decay=0.75, mask=x.mask, workspace=self.ws)
+            plan.cache_compact(self.c, self.k, x.page, x.dtable, src, two, dst0=self.lens, scores=self.scores)
+            self.lens.add_(2)
+            plan.evict_select(self.scores, self.lens, 4, 16, self.kept, self.lens)
+            plan.cache_compact(self.c, self.k, x.page, x.dtable, self.kept, self.lens, scores=self.scores)
+
+        def all(self):
+            torch.cuda.synchronize()
+            ok(plan)
+            bits = torch.int16 if x.dt == torch.bfloat16 else torch.int32
+            return [t.clone() for t in (self.out, self.lse, self.scores, self.kept, self.lens, self.c.view(bits), self.k.view(bits))]
+
+    a, b = State(), State()
+    want = []
+    for q in host:
+        a.reset()
+        a.step(q)
+        want.append(a.all())
+    pinned = host[0].clone().pin_memory()
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        b.step(pinned)
+    for q, w in ((host[0], want[0]), (host[1], want[1]), (host[0], want[0])):
+        torch.cuda.synchronize()
+        pinned.copy_(q)
+        b.reset()
+        g.replay()
+        for got, expected in zip(b.all(), w):
+            assert torch.equal(got, expected)
+
+
+@pytest.mark.parametrize("force", [False, True], ids=["auto", "simt"])
+@pytest.mark.parametrize("B,H,T", [(65535, 1, 1), (2, 4096, 3), (1, 4096, 64)])
+def test_the_largest_batches_and_head_counts(B, H, T, force):
+    """As many sequences, and as many heads, as the calls take: a few tokens each, against plain torch in 64 bits.
+    Bounds as in tree_reference.py, with the batch's largest sum |q k|; the logits stay below 20."""
+    g = torch.Generator(device="cuda").manual_seed(B + T)
+    cap = T + 3
+    r = torch.Generator().manual_seed(B + T)
+    lens = torch.randint(0, 4, (B,), generator=r).int().cuda()
+    c = torch.randn(B * cap, 512, generator=g, device="cuda").clamp(-6, 6).bfloat16()
+    k = torch.randn(B * cap, 64, generator=g, device="cuda").bfloat16()
+    q_c = (torch.randn(B, T, H, 512, generator=g, device="cuda") * 0.08).bfloat16()
+    q_r = (torch.randn(B, T, H, 64, generator=g, device="cuda") * 0.08).bfloat16()
+    plan = kvc.Plan(B, H, 512, 64, "bf16", cap)
+    plan.set(kvc.OPT_FORCE_SIMT, int(force))
+    out, lse = torch.zeros_like(q_c), torch.zeros(B, T, H, device="cuda")
+    s = torch.full((B, cap), -77.0, device="cuda")
+    plan.tree_decode(q_c, q_r, c, k, cap, None, lens, out, lse)
+    plan.attn_mass(q_c, q_r, c, k, cap, None, lens, lse, s)
+    ok(plan)
+    pos, node = torch.arange(cap, device="cuda"), torch.arange(T, device="cuda")
+    for b0 in range(0, B, 8192):
+        b1 = min(B, b0 + 8192)
+        C, K = c.view(B, cap, 512)[b0:b1].double(), k.view(B, cap, 64)[b0:b1].double()
+        n = lens[b0:b1, None, None].long()
+        sees = pos[None, None, :] <= n + node[None, :, None]               # a chain, [b, T, cap]
+        mass = torch.zeros(b1 - b0, cap, dtype=torch.float64, device="cuda")
+        for i in range(T):
+            x = q_c[b0:b1, i].double() @ C.transpose(1, 2) + q_r[b0:b1, i].double() @ K.transpose(1, 2)
+            x = x.masked_fill(~sees[:, i, None, :], -float("inf"))
+            z = torch.logsumexp(x, 2)
+            p = torch.exp(x - z[..., None])
+            want = p @ C
+            ex = 576 * 2.0 ** -23 * float((q_c[b0:b1, i].double().abs() @ C.abs().transpose(1, 2)
+                                           + q_r[b0:b1, i].double().abs() @ K.abs().transpose(1, 2)).max())
+            assert float((lse[b0:b1, i] - z).abs().max()) <= ex + 2.0 ** -20 * 21
+            most = (2 * ex + 2.0 ** -18 + 2.0 ** -8) * (p @ C.abs()) + 2.0 ** -8 * want.abs()
+            assert bool(((out[b0:b1, i].double() - want).abs() <= most).all())
+            mass += torch.exp(x - lse[b0:b1, i].double()[..., None]).sum(1)
+        valid = pos[None, :] < lens[b0:b1, None] + T
+        err = (s[b0:b1].double() - mass).abs()
+        assert bool((err[valid] <= (ex + 2.0 ** -18 + (T * H + 32) * 2.0 ** -23) * mass[valid] + 1e-30).all())
+        assert bool((s[b0:b1][~valid] == -77.0).all())
+
+
+@pytest.mark.parametrize("H,dtype", [(16, "bf16"), (4, "f32")])
+def test_sequences_that_share_their_first_pages(H, dtype):
+    """A common prompt: two pages listed by all three sequences.  Attention and weights read them; an eviction that
+    keeps them where they are may move the rows behind."""
+    kw = {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    x = Batch(H, 3, [300, 200, 450], page=64, seed=59, dtype=dtype, **kw)
+    x.table[1:, :2] = x.table[0, :2]
+    x.dtable.copy_(torch.from_numpy(x.table))
+    x.rows_of = [x.rows(b, np.arange(n + 3)) for b, n in enumerate(x.lens)]
+    plan = x.plan()
+    out, lse = x.decode(plan)
+    check_tree(x, out, lse, tc=dtype == "bf16")
+    s = x.mass(plan, lse, None, 1.0)
+    check_mass(x, s, lse, None, 1.0)
+    kept, kl = torch.zeros(3, 160, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    plan.evict_select(s, x.dlens, 128, 8, kept, kl)
+    before = [x.c[torch.from_numpy(x.rows_of[b]).cuda()].clone() for b in range(3)]
+    plan.cache_compact(x.c, x.k, 64, x.dtable, kept, kl, scores=s)
+    ok(plan)
+    for b in range(3):
+        now = x.c[torch.from_numpy(x.rows_of[b][:160]).cuda()]
+        assert torch.equal(now, before[b][kept[b].long()])
