@@ -49,8 +49,9 @@ typedef enum {
     LCA_ERR_NO_MEMORY = 7,       /* device or host allocation failed */
     LCA_ERR_DEVICE_CHECK = 8,    /* debug build only: a kernel index failed its range check and the
                                     access was skipped (see lca_get_device_error) */
-    LCA_ERR_DEVICE_INPUT = 9     /* lca_decode_paged: a length or block-table entry read on the
-                                    device was out of range (see lca_get_device_error) */
+    LCA_ERR_DEVICE_INPUT = 9     /* a length, block-table entry or list of rows read on the device
+                                    was out of range (lca_decode_paged, the draft-tree and eviction
+                                    calls; see lca_get_device_error) */
 } lca_status;
 
 typedef enum { LCA_F32 = 0, LCA_BF16 = 1 } lca_dtype;

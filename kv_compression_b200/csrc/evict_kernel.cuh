@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kSelectThreads) lca_select_kernel(const Select
 // For the same reason the next tile's reads may be under way while this tile is
 // written, so two tiles (16 reads of 16 bytes a thread) are in flight.
 //
-// It is bound by memory latency with few sequences and comes to 4.8 TB/s, read
-// and written, with 64.  Wide strips suit DRAM and L2, but a block for each SM
+// It is bound by memory latency with few sequences and comes to 5.2 TB/s, read
+// and written, with 64 (8192 of 32768 rows each: 231 us).  Wide strips suit DRAM and L2, but a block for each SM
 // comes first: narrow ones as long as an SM gets no second block (4 sequences,
 // 16384 of 32768 rows each: 49 us, 61 with wide ones; 8 sequences, 8192 rows: 57,
 // wide 41), and 512 threads instead of 256 as long as all wide ones are resident
