@@ -453,3 +453,26 @@ def test_sequences_that_share_their_first_pages(H, dtype):
     for b in range(3):
         now = x.c[torch.from_numpy(x.rows_of[b][:160]).cuda()]
         assert torch.equal(now, before[b][kept[b].long()])
+
+
+@pytest.mark.parametrize("H,dtype,force", KINDS)
+def test_what_belongs_to_no_drafted_token_is_not_felt(H, dtype, force):
+    """Queries, mask words and lse of nodes past a sequence's own, and old sums past its cached tokens, may hold anything."""
+    kw = {} if dtype == "bf16" else dict(d_c=64, d_r=16)
+    drafts = [3, 7, 0, 1, 8]
+    x = Batch(H, 8, [300, 127, 64, 0, 513], drafts, page=64, seed=60, dtype=dtype, **kw)
+    plan = x.plan()
+    plan.set(kvc.OPT_FORCE_SIMT, int(force))
+    prev = torch.rand(5, x.cap, device="cuda")
+    out, lse = x.decode(plan)
+    s = x.mass(plan, lse, prev, 0.5)
+    for b, d in enumerate(drafts):
+        x.q_c[b, d:], x.q_r[b, d:] = float("nan"), float("inf")
+        x.mask[b, d:] = -1
+        lse[b, d:] = float("nan")
+        prev[b, x.lens[b]:] = float("nan")
+    again, z = x.decode(plan)
+    assert torch.equal(again, out)
+    assert all(torch.equal(z[b, :d], lse[b, :d]) for b, d in enumerate(drafts))
+    assert torch.equal(x.mass(plan, lse, prev, 0.5), s)
+    ok(plan)
