@@ -47,9 +47,11 @@ L2_BYTES = 126 * 1024 * 1024
 _CSRC = "kv_compression_b200/csrc/"
 TRAFFIC_FILES = {
     "v2lite": ("profiles/lca_tc_kernel_v2lite_traffic.txt",
-               [_CSRC + "tc_kernel.cuh", _CSRC + "ptx.cuh", _CSRC + "checks.cuh", _CSRC + "paged_kernel.cuh"]),
+               [_CSRC + "tc_kernel.cuh", _CSRC + "ptx.cuh", _CSRC + "checks.cuh", _CSRC + "paged_kernel.cuh",
+                _CSRC + "device_input.cuh"]),
     "v2": ("profiles/lca_pair_kernel_v2_traffic.txt",
-           [_CSRC + "pair_kernel.cuh", _CSRC + "ptx.cuh", _CSRC + "checks.cuh", _CSRC + "paged_kernel.cuh"]),
+           [_CSRC + "pair_kernel.cuh", _CSRC + "ptx.cuh", _CSRC + "checks.cuh", _CSRC + "paged_kernel.cuh",
+            _CSRC + "device_input.cuh"]),
 }
 MAIN_KERNEL_NAMES = {"tcgen05": "lca_tc_kernel", "tcgen05_pair": "lca_pair_kernel", "simt": "lca_simt_kernel"}
 
